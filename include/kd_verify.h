@@ -79,6 +79,7 @@ typedef uint16_t kd_bf16_t;
 #define KD_DEV_TIMEOUT       0x10  /* a bounded wait inside a kernel gave up            */
 #define KD_DEV_BAD_MASK      0x20  /* a node's mask lacks bit 0 (root) or its own bit   */
 #define KD_DEV_BAD_PAGE      0x40  /* a paged cache's page id is outside the page pool  */
+#define KD_DEV_BAD_SEQLENS   0x80  /* cumulative lengths negative, decreasing or beyond the rows given */
 
 #define KD_D_C 512
 #define KD_D_R 64
@@ -361,6 +362,204 @@ int kd_kv_compact_paged(kd_bf16_t* c_pages, kd_bf16_t* r_pages, int64_t kv_row_s
                         int64_t pages_per_req, int64_t num_pages, const int32_t* path,
                         const int32_t* len, int32_t* cache_lens, int B, int n, int32_t* dev_error,
                         cudaStream_t stream);
+
+/*
+ * ------------------------------------------------------------------------------
+ * Operators next to the verify step: what produces the queries and the cache rows
+ * (kd_qk_norm_rope, kd_kv_norm_rope_write), the attention that reads a prompt
+ * (kd_prompt_attn), and what bounds a cache's length (kd_kv_attn_weights,
+ * kd_kv_evict).  Position rotations read a table of cosines and sines:
+ *   rope_table [max_pos][rot] fp32: row p holds cos(p f_i) for i < rot/2, then
+ *   sin(p f_i); f_i are the model's inverse frequencies, whatever its scaling.
+ *   A rotation by position p takes the pair (x, y) of index i to
+ *   (x cos - y sin, x sin + y cos); pair i is elements (i, i + rot/2) of the rotated
+ *   range, or (2i, 2i + 1) with interleaved != 0.
+ *   A position outside [0, max_pos) sets KD_DEV_BAD_POSITION and that token is skipped.
+ * Packed sequences are given by cumulative lengths cu [B+1] int32 (device), cu[0] = 0:
+ * sequence b is rows cu[b] .. cu[b+1]-1 (a length of 0 is allowed); rows from cu[B] on
+ * belong to no sequence and are left as they are.
+ * Norms, rotations, softmax statistics and weights are computed in fp32 and rounded
+ * once, to the type of the output.
+ */
+
+/*
+ * kd_qk_norm_rope -- RMS norm of every query and key head, then the rotation of
+ * `rot` of its elements, one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (over the head's D elements)
+ *   out = y with elements [rot_offset, rot_offset + rot) rotated by positions[t].
+ *   q [T][H][D], k [T][Hk][D] bf16 with token and head strides in elements (unit
+ *   stride inside a head); k may be NULL with Hk = 0.  q_weight, k_weight [D] bf16,
+ *   each NULL for no norm (rotation only).  q_out, k_out: the same shapes, their own
+ *   strides; out may be exactly its input (same pointer and strides), and must not
+ *   overlap it otherwise.
+ * Limits: T >= 0 (0 enqueues nothing), 1 <= H, 0 <= Hk, T (H + Hk) <= 2^31 - 1; D a
+ * multiple of 8, 16 <= D <= 256; rot a multiple of 16, 16 <= rot; rot_offset a
+ * multiple of 8 with rot_offset + rot <= D; eps >= 0; pointers 16-byte aligned and
+ * strides multiples of 8.
+ */
+int kd_qk_norm_rope(const kd_bf16_t* q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const kd_bf16_t* k, int64_t k_tok_stride, int64_t k_head_stride,
+                    const kd_bf16_t* q_weight, const kd_bf16_t* k_weight, float eps,
+                    const float* rope_table, int64_t max_pos, const int32_t* positions,
+                    int T, int H, int Hk, int D, int rot, int rot_offset, int interleaved,
+                    kd_bf16_t* q_out, int64_t qo_tok_stride, int64_t qo_head_stride,
+                    kd_bf16_t* k_out, int64_t ko_tok_stride, int64_t ko_head_stride,
+                    int32_t* dev_error, cudaStream_t stream);
+
+/*
+ * kd_kv_norm_rope_write -- the cache rows of T new tokens from the down-projection's
+ * output, and their queries' rope parts, in one launch: what kd_kv_write_nodes does
+ * for latents that are ready, from latents that are not.  Token i of request b goes
+ * to slot cache_lens[b] + i:
+ *   c_kv[slot]   = kv[t][0..511] / sqrt(mean(kv[t][0..511]^2) + eps) * kv_weight
+ *   k_rope[slot] = kv[t][512..575] rotated by the token's position
+ *   q_rope_out[t][h] = q_rope_in[t][h] rotated by the token's position
+ *   kv [T][576] bf16, row stride kv_row_stride; kv_weight [512] bf16 or NULL (no norm).
+ *   cu_seqlens [B+1], or NULL for T / B tokens per request (T a multiple of B; any
+ *   number per request, not only a tree's).  positions [T] int32, or NULL for
+ *   cache_lens[b] + i.  rope_table has rot = 64.
+ *   q_rope_in [T][H][64] bf16 with token and head strides, q_rope_out [T][H][64]
+ *   contiguous; both NULL with H = 0 to write the cache alone.  q_rope_out may be
+ *   q_rope_in when that is contiguous.
+ * cache_lens is not changed.  A request with cache_lens + length > cap (or < 0) sets
+ * KD_DEV_CACHE_FULL and none of its rows is written; a bad cu_seqlens sets
+ * KD_DEV_BAD_SEQLENS and its tokens are skipped.  The queries' part does not depend on
+ * the cache: it is written for every token of a sequence with a valid position.
+ * Limits: T >= 0, B >= 1, 0 <= H <= 128; alignment as kd_kv_write_nodes, strides
+ * multiples of 8.
+ * The paged form writes through a page table (any page_size >= 1); a token whose page
+ * id lies outside the pool sets KD_DEV_BAD_PAGE and is not written.
+ */
+int kd_kv_norm_rope_write(kd_bf16_t* c_kv, kd_bf16_t* k_rope, int64_t kv_row_stride_c,
+                          int64_t kv_row_stride_r, int64_t cap, const int32_t* cache_lens,
+                          const kd_bf16_t* kv, int64_t kv_row_stride, const kd_bf16_t* kv_weight,
+                          float eps, const float* rope_table, int64_t max_pos,
+                          const int32_t* positions, int interleaved, const int32_t* cu_seqlens,
+                          int B, int T, const kd_bf16_t* q_rope_in, int64_t q_tok_stride,
+                          int64_t q_head_stride, int H, kd_bf16_t* q_rope_out,
+                          int32_t* dev_error, cudaStream_t stream);
+int kd_kv_norm_rope_write_paged(kd_bf16_t* c_pages, kd_bf16_t* r_pages, int64_t kv_row_stride_c,
+                                int64_t kv_row_stride_r, int page_size, const int32_t* page_table,
+                                int64_t pages_per_req, int64_t num_pages, const int32_t* cache_lens,
+                                const kd_bf16_t* kv, int64_t kv_row_stride,
+                                const kd_bf16_t* kv_weight, float eps, const float* rope_table,
+                                int64_t max_pos, const int32_t* positions, int interleaved,
+                                const int32_t* cu_seqlens, int B, int T, const kd_bf16_t* q_rope_in,
+                                int64_t q_tok_stride, int64_t q_head_stride, int H,
+                                kd_bf16_t* q_rope_out, int32_t* dev_error, cudaStream_t stream);
+
+/*
+ * kd_prompt_attn -- causal attention of whole prompts, packed, with grouped heads
+ * (the per-head form of the attention, for prompts whose keys and values have been
+ * up-projected; kd_tree_verify_attn is the absorb form that single tokens, trees and
+ * chunks use over the latent cache).  Head h reads key head h / (H / Hk).  For row i of
+ * sequence b with nq queries and nk keys (its queries are the last nq of the nk
+ * positions), over j <= i + nk - nq, 0 <= j < nk:
+ *   s_j = scale (q_nope[i][h] . k_nope[j][g] + q_rope[i][h] . k_rope[j][g])
+ *   out[i][h] = sum_j softmax(s)_j v[j][g],  lse[i][h] = ln sum_j exp(s_j)
+ *   A row without keys (nk < nq) gets out = 0 and lse = -inf.
+ *   q_nope [T][H][128], q_rope [T][H][64], k_nope, v [Tk][Hk][128], k_rope [Tk][Hk][64]
+ *   bf16, each with a token and a head stride in elements; k_head_stride of k_rope 0
+ *   means one rope key for all heads.  q_rope and k_rope both NULL: no rope part.
+ *   cu_seqlens_q [B+1]; cu_seqlens_k [B+1] or NULL (the queries' own).
+ *   out [T][H][128] bf16, lse [T][H] fp32, contiguous, not overlapping an input.
+ * The keys and values of other sequences never enter a row, NaN or infinite ones
+ * included, nor do the keys of later positions.  (A NaN or infinite v of a later position
+ * of the row's own sequence can: it meets the weight 0 in the product.)  A sequence whose cumulative lengths are bad sets KD_DEV_BAD_SEQLENS and
+ * its rows are left as they are.
+ * Limits: T, Tk >= 0 (T = 0 enqueues nothing), T H and Tk Hk <= 2^31 - 1,
+ * 1 <= B <= 65535, 1 <= H <= 128, Hk divides H, scale > 0; pointers 16-byte aligned,
+ * strides multiples of 8.
+ */
+int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qn_tok_stride, int64_t qn_head_stride,
+                   const kd_bf16_t* q_rope, int64_t qr_tok_stride, int64_t qr_head_stride,
+                   const kd_bf16_t* k_nope, int64_t kn_tok_stride, int64_t kn_head_stride,
+                   const kd_bf16_t* k_rope, int64_t kr_tok_stride, int64_t kr_head_stride,
+                   const kd_bf16_t* v, int64_t v_tok_stride, int64_t v_head_stride,
+                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int T, int Tk,
+                   int H, int Hk, float scale, kd_bf16_t* out, float* lse, int32_t* dev_error,
+                   cudaStream_t stream);
+
+/*
+ * kd_kv_attn_weights -- the attention weight each cache slot receives, added to what
+ * it had: the measure by which kd_kv_evict chooses.  With the lse that
+ * kd_tree_verify_attn returned for the same q_nope_absorbed, q_rope, cache and vis,
+ * and the nodes counted being path[b][0 .. len[b]-1] (kd_tree_accept's, so that
+ * rejected drafts leave no trace), or every node when path and len are NULL:
+ *   col_j = sum over counted nodes i that see slot j, and heads h, of
+ *           exp(s_ihj - lse[b][i][h])               (s as in kd_tree_verify_attn)
+ *   weights_out[b][j]     = weights_in[b][j] + col_j         for j < L = cache_lens[b]
+ *   weights_out[b][L + m] = col_{L + path[b][m]}             for m < len[b]
+ * that is, the new slots' weights are stored in the order kd_kv_compact will give the
+ * slots: call it between kd_tree_accept and kd_kv_compact.  Entries from L + len on are
+ * left as they are.  A counted row whose lse is -inf adds nothing.
+ *   weights_in [B][w_in_stride] fp32 or NULL (zeros), weights_out [B][w_out_stride]
+ *   fp32, strides >= cap; weights_out may be weights_in (same stride).
+ * Sums run in a fixed order: the same call gives the same bits.  A request with
+ * cache_lens + n > cap (or < 0) sets KD_DEV_CACHE_FULL; len not in [1, n] or a path
+ * entry outside [0, n) sets KD_DEV_BAD_PATH; (paged) a page id outside the pool among
+ * its first ceil((L + n) / page_size) sets KD_DEV_BAD_PAGE: nothing of it is written.
+ * Layouts, limits and alignment of the other arguments as kd_tree_verify_attn; the
+ * paged form takes page_size 64, 128 or 256.
+ */
+int kd_kv_attn_weights(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* q_rope,
+                       const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t kv_row_stride_c,
+                       int64_t kv_row_stride_r, int64_t cap, const int32_t* cache_lens,
+                       const uint32_t* vis, const float* lse, const int32_t* path,
+                       const int32_t* len, int B, int n, int H, float scale,
+                       const float* weights_in, int64_t w_in_stride, float* weights_out,
+                       int64_t w_out_stride, int32_t* dev_error, cudaStream_t stream);
+int kd_kv_attn_weights_paged(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* q_rope,
+                             const kd_bf16_t* c_pages, const kd_bf16_t* r_pages,
+                             int64_t kv_row_stride_c, int64_t kv_row_stride_r, int page_size,
+                             const int32_t* page_table, int64_t pages_per_req, int64_t num_pages,
+                             const int32_t* cache_lens, const uint32_t* vis, const float* lse,
+                             const int32_t* path, const int32_t* len, int B, int n, int H,
+                             float scale, const float* weights_in, int64_t w_in_stride,
+                             float* weights_out, int64_t w_out_stride, int32_t* dev_error,
+                             cudaStream_t stream);
+
+/*
+ * kd_kv_evict -- cuts every request's cache down to at most `keep` slots.  A request
+ * with L = cache_lens[b] <= keep keeps all of them; a longer one keeps its first `sink`
+ * slots, its last `recent` slots and, of those between, the keep - sink - recent with
+ * the largest weights_in (equal weights: the lower slot; NaN below every number, -0
+ * equal to +0).  The kept slots' rows and weights go to slots 0, 1, ... of the
+ * destination in their old order:
+ *   kept [B][keep] int32 out: the kept slots, ascending, then -1.
+ *   c_dst, r_dst[b][m] = row kept[b][m] of c_kv, k_rope; weights_out[b][m] =
+ *   weights_in[b][kept[b][m]]; lens_out[b] = min(L, keep).
+ * Destination rows and weights from lens_out on are left as they are.
+ *   The destination is another cache (its own strides and dst_cap; it must not overlap
+ *   the source) or the source itself: c_dst == c_kv, r_dst == k_rope with the same
+ *   strides and dst_cap == cap.  lens_out may be cache_lens, weights_out may be
+ *   weights_in (same stride).
+ * Keys carry their rotation with them: later tokens go on with their own positions,
+ * which are then no longer cache_lens + i.
+ * A request with L < 0, L > cap or lens_out > dst_cap sets KD_DEV_CACHE_FULL; its kept
+ * row is -1 and nothing else of it is written.
+ * Limits: keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep, cap <= 2^31 - 1.
+ * The paged form goes through page tables (any page_size >= 1, the same for both): in
+ * place when the destination's pools and table are the source's, else the
+ * destination's pages must be none of the source's.  A page id outside its pool among
+ * the slots read or written sets KD_DEV_BAD_PAGE, and the request is treated as above.
+ */
+int kd_kv_evict(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t kv_row_stride_c,
+                int64_t kv_row_stride_r, int64_t cap, const int32_t* cache_lens,
+                const float* weights_in, int64_t w_in_stride, int keep, int sink, int recent, int B,
+                kd_bf16_t* c_dst, kd_bf16_t* r_dst, int64_t dst_row_stride_c,
+                int64_t dst_row_stride_r, int64_t dst_cap, float* weights_out,
+                int64_t w_out_stride, int32_t* lens_out, int32_t* kept, int32_t* dev_error,
+                cudaStream_t stream);
+int kd_kv_evict_paged(const kd_bf16_t* c_pages, const kd_bf16_t* r_pages, int64_t kv_row_stride_c,
+                      int64_t kv_row_stride_r, int page_size, const int32_t* page_table,
+                      int64_t pages_per_req, int64_t num_pages, const int32_t* cache_lens,
+                      const float* weights_in, int64_t w_in_stride, int keep, int sink, int recent,
+                      int B, kd_bf16_t* c_dst, kd_bf16_t* r_dst, int64_t dst_row_stride_c,
+                      int64_t dst_row_stride_r, const int32_t* dst_page_table,
+                      int64_t dst_pages_per_req, int64_t dst_num_pages, float* weights_out,
+                      int64_t w_out_stride, int32_t* lens_out, int32_t* kept, int32_t* dev_error,
+                      cudaStream_t stream);
 
 /*
  * kd_read_device_error -- synchronises `stream`, returns the device error word

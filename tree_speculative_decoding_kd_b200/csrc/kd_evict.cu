@@ -1,0 +1,325 @@
+// Eviction by accumulated attention weight: a request's cache cut down to its first
+// `sink` slots, its last `recent` slots and the slots of the largest weights between.
+//
+// Two launches.  select_kernel (one CTA per request) finds the weight of the last slot
+// that is kept, by a radix selection over order-preserving 32-bit keys (11 + 11 + 10
+// bits, a histogram in shared memory each), and then walks the slots in order once,
+// numbering the kept ones: equal weights are taken from the lowest slot.  The move
+// copies the kept rows: bound by memory, 2 x 1152 bytes a row, 16 bytes per lane.
+
+#include "kd_common.cuh"
+#include "kd_slots.cuh"
+
+namespace kd {
+namespace ev {
+
+constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int BINS = 2048;
+constexpr int PER = 4;                       // neighbouring slots a thread numbers per step
+
+// Unsigned key in the order of the weights: NaN lowest, -0 equal to +0.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);        // -0 + 0 = +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct SelectParams {
+  const int32_t* lens;
+  const float* w_in;
+  float* w_out;
+  int32_t *lens_out, *kept, *err;
+  SlotMap src, dst;
+  int64_t wi, wo;
+  int keep, sink, recent;
+};
+
+// Inclusive sum over the block of one value per thread; `warp_sums` [WARPS].
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  if (lane == 31) warp_sums[w] = v;
+  __syncthreads();
+  uint32_t s = warp_sums[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += o;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, s, w ? w - 1 : 0);
+  __syncthreads();                                    // warp_sums may be written again
+  return v + (w ? before : 0u);
+}
+
+__global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
+  __shared__ uint32_t hist[BINS];
+  __shared__ uint32_t warp_sums[WARPS];
+  __shared__ uint32_t found[2];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int64_t L64 = p.lens[b];
+  int32_t* kept = p.kept + (size_t)b * p.keep;
+  const int64_t fit = L64 < p.keep ? L64 : p.keep;
+  int bad = 0;
+  if (L64 < 0 || L64 > p.src.cap || fit > p.dst.cap) bad = KD_DEV_CACHE_FULL;
+  if (!bad && p.src.pt) {                              // pages of every slot read or written
+    bool out = false;
+    for (int64_t q = tid; q * p.src.P < L64; q += THREADS)
+      out |= !p.src.pages_ok(b, q * p.src.P, q * p.src.P + 1);
+    for (int64_t q = tid; q * p.dst.P < fit; q += THREADS)
+      out |= !p.dst.pages_ok(b, q * p.dst.P, q * p.dst.P + 1);
+    if (__syncthreads_or(out)) bad = KD_DEV_BAD_PAGE;
+  }
+  if (bad) {
+    if (tid == 0) raise_dev_error(p.err, bad);
+    for (int m = tid; m < p.keep; m += THREADS) kept[m] = -1;
+    return;
+  }
+  const int L = (int)L64, first = p.sink, last = L - p.recent;
+  const float* w = p.w_in + (int64_t)b * p.wi;
+  uint32_t thr = 0, need = 0;                          // keys above thr are kept, and `need` equal to it
+  if (L > p.keep) {
+    need = (uint32_t)(p.keep - p.sink - p.recent);
+    uint32_t mask = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && need; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      for (int i = tid; i < BINS; i += THREADS) hist[i] = 0u;
+      __syncthreads();
+      for (int j0 = first; j0 < last; j0 += THREADS) {
+        const int j = j0 + tid;
+        const uint32_t key = j < last ? order_key(w[j]) : 0u;
+        const bool in = j < last && (key & mask) == (thr & mask);
+        const uint32_t d = in ? (key >> shift) & digits : BINS;
+        // weights of one magnitude share a digit: one atomic per digit and warp
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (in && (tid & 31) == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
+      }
+      __syncthreads();
+      // thread t holds the bins 2047 - 2t and 2046 - 2t: sums run from the largest digit
+      const uint32_t h1 = hist[BINS - 1 - 2 * tid], h0 = hist[BINS - 2 - 2 * tid];
+      uint32_t total;
+      const uint32_t upto = block_scan(h1 + h0, warp_sums, total), above = upto - h1 - h0;
+      if (above < need && upto >= need) {
+        const bool hi = above + h1 >= need;
+        found[0] = (uint32_t)(hi ? BINS - 1 - 2 * tid : BINS - 2 - 2 * tid);
+        found[1] = need - (hi ? above : above + h1);
+      }
+      __syncthreads();
+      thr |= found[0] << shift;
+      need = found[1];
+      mask |= digits << shift;
+      __syncthreads();
+    }
+  }
+  const bool all = L <= p.keep, none = !all && p.keep == p.sink + p.recent;
+  float* wo = p.w_out + (int64_t)b * p.wo;
+  uint32_t taken = 0, equal = 0;                       // before this step: above or forced, and equal
+  for (int j0 = 0; j0 < L; j0 += THREADS * PER) {
+    float v[PER];
+    uint32_t kind[PER], mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = j0 + tid * PER + i;
+      v[i] = j < L ? w[j] : 0.f;
+      kind[i] = 0;
+      if (j < L) {
+        const uint32_t key = order_key(v[i]);
+        if (all || j < first || j >= last || (!none && key > thr)) kind[i] = 1u << 16;
+        else if (!none && key == thr) kind[i] = 1u;
+      }
+      mine += kind[i];
+    }
+    uint32_t total;
+    uint32_t at = block_scan(mine, warp_sums, total) - mine;   // all reads of this step are done
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t a = taken + (at >> 16), e = equal + (at & 0xFFFFu);
+      if (kind[i] == 1u << 16 || (kind[i] == 1u && e < need)) {
+        const uint32_t m = a + (e < need ? e : need);
+        kept[m] = j0 + tid * PER + i;
+        wo[m] = v[i];
+      }
+      at += kind[i];
+    }
+    taken += total >> 16;
+    equal += total & 0xFFFFu;
+  }
+  for (int m = (int)fit + tid; m < p.keep; m += THREADS) kept[m] = -1;
+  if (tid == 0) p.lens_out[b] = (int32_t)fit;
+}
+
+struct MoveParams {
+  const uint4 *c, *r;
+  uint4 *cd, *rd;
+  const int32_t* kept;
+  SlotMap src, dst;
+  int64_t sc, sr, dc, dr;          // row strides in 16-byte units
+  int keep;
+};
+constexpr int CC = KD_D_C / 8, CR = KD_D_R / 8;    // 16-byte pieces of a row
+
+// Another destination: a warp copies ROWS rows, all their loads in flight together.
+constexpr int ROWS = 4;
+__global__ void __launch_bounds__(256) move_kernel(const MoveParams p) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int m0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
+  const int32_t* kept = p.kept + (size_t)b * p.keep;
+  uint4 v[ROWS][2], x[ROWS];
+  bool on[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int s = m0 + i < p.keep ? kept[m0 + i] : -1;
+    on[i] = s >= 0;
+    if (!on[i]) continue;
+    const int64_t row = p.src.row(b, s);
+    v[i][0] = __ldcs(p.c + row * p.sc + lane);
+    v[i][1] = __ldcs(p.c + row * p.sc + lane + 32);
+    if (lane < CR) x[i] = __ldcs(p.r + row * p.sr + lane);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (!on[i]) continue;
+    const int64_t row = p.dst.row(b, m0 + i);
+    p.cd[row * p.dc + lane] = v[i][0];
+    p.cd[row * p.dc + lane + 32] = v[i][1];
+    if (lane < CR) p.rd[row * p.dr + lane] = x[i];
+  }
+}
+
+// In place: a CTA takes one 64-byte column slice of every row (four 16-byte pieces; 16
+// slices of the latent, 2 of the rope key), so that rows of one slice move in order while
+// the slices need no order between them.  Rows move down (kept[m] >= m, ascending): once
+// the sources of rows [m0, m1) are read, nothing that is still to be read lies below row
+// m1, so each step reads its rows, waits for the whole CTA to have read, and writes.
+constexpr int SLICES = (CC + CR) / 4, STEP = 8;
+__global__ void __launch_bounds__(512) move_inplace_kernel(const MoveParams p) {
+  const int b = blockIdx.y, sl = blockIdx.x, piece = threadIdx.x & 3, r = threadIdx.x >> 2;
+  const int32_t* kept = p.kept + (size_t)b * p.keep;
+  const bool lat = sl < CC / 4;
+  uint4* base = lat ? p.cd + sl * 4 + piece : p.rd + (sl - CC / 4) * 4 + piece;
+  const int64_t stride = lat ? p.dc : p.dr;
+  for (int m0 = 0; m0 < p.keep; m0 += 128 * STEP) {
+    uint4 v[STEP];
+    int s[STEP];
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+      const int m = m0 + i * 128 + r;
+      s[i] = m < p.keep ? kept[m] : -1;
+      if (s[i] == m) s[i] = -1;                        // already in place
+      if (s[i] >= 0) v[i] = base[p.src.row(b, s[i]) * stride];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < STEP; ++i)
+      if (s[i] >= 0) base[p.dst.row(b, m0 + i * 128 + r) * stride] = v[i];
+  }
+}
+
+}  // namespace ev
+}  // namespace kd
+
+using namespace kd;
+
+// ================================================================== C ABI
+static int evict_impl(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc, int64_t sr, const SlotMap& src,
+                      const int32_t* cache_lens, const float* w_in, int64_t wi, int keep, int sink, int recent, int B,
+                      kd_bf16_t* c_dst, kd_bf16_t* r_dst, int64_t dc, int64_t dr, const SlotMap& dst, bool inplace,
+                      float* w_out, int64_t wo, int32_t* lens_out, int32_t* kept, int32_t* dev_error,
+                      cudaStream_t stream) {
+  if (!cache_ok(c_kv, k_rope, sc, sr, src.cap) || !cache_ok(c_dst, r_dst, dc, dr, dst.cap) || !cache_lens || !w_in ||
+      !w_out || !lens_out || !kept || B < 1 || B > 65535 || keep < 1 || sink < 0 || recent < 0 ||
+      (int64_t)sink + recent > keep || src.cap > INT32_MAX || dst.cap > INT32_MAX || wi < src.cap ||
+      wo < (dst.cap < keep ? dst.cap : keep) || (w_out == w_in && wi != wo))
+    return KD_EINVAL;
+  int st = device_sms(nullptr);
+  if (st) return st;
+  ev::SelectParams s;
+  s.lens = cache_lens;
+  s.w_in = w_in;
+  s.w_out = w_out;
+  s.lens_out = lens_out;
+  s.kept = kept;
+  s.err = dev_error;
+  s.src = src;
+  s.dst = dst;
+  s.wi = wi;
+  s.wo = wo;
+  s.keep = keep;
+  s.sink = sink;
+  s.recent = recent;
+  ev::select_kernel<<<B, ev::THREADS, 0, stream>>>(s);
+  if ((st = launch_status("select_kernel"))) return st;
+  ev::MoveParams m;
+  m.c = reinterpret_cast<const uint4*>(c_kv);
+  m.r = reinterpret_cast<const uint4*>(k_rope);
+  m.cd = reinterpret_cast<uint4*>(c_dst);
+  m.rd = reinterpret_cast<uint4*>(r_dst);
+  m.kept = kept;
+  m.src = src;
+  m.dst = dst;
+  m.sc = sc / 8;
+  m.sr = sr / 8;
+  m.dc = dc / 8;
+  m.dr = dr / 8;
+  m.keep = keep;
+  if (inplace)
+    ev::move_inplace_kernel<<<dim3(ev::SLICES, B), 512, 0, stream>>>(m);
+  else
+    ev::move_kernel<<<dim3((unsigned)((keep + 8 * ev::ROWS - 1) / (8 * ev::ROWS)), B), 256, 0, stream>>>(m);
+  return launch_status("move_kernel");
+}
+
+// Whether the memory of two sets of rows (width elements each) meets.
+static bool overlap(const kd_bf16_t* a, int64_t sa, const kd_bf16_t* b, int64_t sb, int width, int64_t na, int64_t nb) {
+  if (na < 1 || nb < 1) return false;
+  const kd_bf16_t *ea = a + (na - 1) * sa + width, *eb = b + (nb - 1) * sb + width;
+  return a < eb && b < ea;
+}
+
+extern "C" int kd_kv_evict(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc, int64_t sr, int64_t cap,
+                           const int32_t* cache_lens, const float* weights_in, int64_t w_in_stride, int keep, int sink,
+                           int recent, int B, kd_bf16_t* c_dst, kd_bf16_t* r_dst, int64_t dst_row_stride_c,
+                           int64_t dst_row_stride_r, int64_t dst_cap, float* weights_out, int64_t w_out_stride,
+                           int32_t* lens_out, int32_t* kept, int32_t* dev_error, cudaStream_t stream) {
+  const bool c_same = c_dst == c_kv, r_same = r_dst == k_rope;
+  if (c_same != r_same || (c_same && (dst_row_stride_c != sc || dst_row_stride_r != sr || dst_cap != cap)))
+    return KD_EINVAL;
+  if (!c_same && B >= 1 && (overlap(c_kv, sc, c_dst, dst_row_stride_c, KD_D_C, B * cap, B * dst_cap) ||
+                            overlap(k_rope, sr, r_dst, dst_row_stride_r, KD_D_R, B * cap, B * dst_cap)))
+    return KD_EINVAL;
+  return evict_impl(c_kv, k_rope, sc, sr, SlotMap{nullptr, cap, 0, 1, 0}, cache_lens, weights_in, w_in_stride, keep,
+                    sink, recent, B, c_dst, r_dst, dst_row_stride_c, dst_row_stride_r,
+                    SlotMap{nullptr, dst_cap, 0, 1, 0}, c_same, weights_out, w_out_stride, lens_out, kept, dev_error,
+                    stream);
+}
+
+extern "C" int kd_kv_evict_paged(const kd_bf16_t* c_pages, const kd_bf16_t* r_pages, int64_t sc, int64_t sr,
+                                 int page_size, const int32_t* page_table, int64_t pages_per_req, int64_t num_pages,
+                                 const int32_t* cache_lens, const float* weights_in, int64_t w_in_stride, int keep,
+                                 int sink, int recent, int B, kd_bf16_t* c_dst, kd_bf16_t* r_dst,
+                                 int64_t dst_row_stride_c, int64_t dst_row_stride_r, const int32_t* dst_page_table,
+                                 int64_t dst_pages_per_req, int64_t dst_num_pages, float* weights_out,
+                                 int64_t w_out_stride, int32_t* lens_out, int32_t* kept, int32_t* dev_error,
+                                 cudaStream_t stream) {
+  if (!paged_ok(page_table, page_size, pages_per_req, num_pages) ||
+      !paged_ok(dst_page_table, page_size, dst_pages_per_req, dst_num_pages))
+    return KD_EINVAL;
+  const bool c_same = c_dst == c_pages, r_same = r_dst == r_pages;
+  const bool table_same = dst_page_table == page_table;
+  if (c_same != r_same || (c_same && (dst_row_stride_c != sc || dst_row_stride_r != sr)) ||
+      (c_same && table_same && (dst_pages_per_req != pages_per_req || dst_num_pages != num_pages)))
+    return KD_EINVAL;
+  return evict_impl(c_pages, r_pages, sc, sr,
+                    SlotMap{page_table, pages_per_req * page_size, num_pages, page_size, (int)pages_per_req},
+                    cache_lens, weights_in, w_in_stride, keep, sink, recent, B, c_dst, r_dst, dst_row_stride_c,
+                    dst_row_stride_r,
+                    SlotMap{dst_page_table, dst_pages_per_req * page_size, dst_num_pages, page_size,
+                            (int)dst_pages_per_req},
+                    c_same && table_same, weights_out, w_out_stride, lens_out, kept, dev_error, stream);
+}

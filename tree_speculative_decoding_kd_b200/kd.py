@@ -47,6 +47,22 @@ _SIGS = {
     "kd_tree_accept_logits": (_i, [_p, _p, _p, _i, _i, _i64, _p, _p, _p, _p, _p, _sz, _p, _p]),
     "kd_kv_compact": (_i, [_p, _p, _i64, _i64, _i64, _p, _p, _p, _i, _i, _p, _p]),
     "kd_kv_write_nodes": (_i, [_p, _p, _i64, _i64, _i64, _p, _p, _p, _i, _i, _p, _p]),
+    "kd_qk_norm_rope": (_i, [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _f, _p, _i64, _p, _i, _i, _i, _i, _i, _i,
+                             _i, _p, _i64, _i64, _p, _i64, _i64, _p, _p]),
+    "kd_kv_norm_rope_write": (_i, [_p, _p, _i64, _i64, _i64, _p, _p, _i64, _p, _f, _p, _i64, _p, _i, _p, _i, _i,
+                                   _p, _i64, _i64, _i, _p, _p, _p]),
+    "kd_kv_norm_rope_write_paged": (_i, [_p, _p, _i64, _i64, _i, _p, _i64, _i64, _p, _p, _i64, _p, _f, _p, _i64,
+                                         _p, _i, _p, _i, _i, _p, _i64, _i64, _i, _p, _p, _p]),
+    "kd_prompt_attn": (_i, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _p,
+                            _i, _i, _i, _i, _i, _f, _p, _p, _p, _p]),
+    "kd_kv_attn_weights": (_i, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _i, _i, _i, _f, _p, _i64, _p,
+                                _i64, _p, _p]),
+    "kd_kv_attn_weights_paged": (_i, [_p, _p, _p, _p, _i64, _i64, _i, _p, _i64, _i64, _p, _p, _p, _p, _p, _i, _i,
+                                      _i, _f, _p, _i64, _p, _i64, _p, _p]),
+    "kd_kv_evict": (_i, [_p, _p, _i64, _i64, _i64, _p, _p, _i64, _i, _i, _i, _i, _p, _p, _i64, _i64, _i64, _p, _i64,
+                         _p, _p, _p, _p]),
+    "kd_kv_evict_paged": (_i, [_p, _p, _i64, _i64, _i, _p, _i64, _i64, _p, _p, _i64, _i, _i, _i, _i, _p, _p, _i64,
+                               _i64, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p]),
     "kd_read_device_error": (_i, [_p, _i, _p]),
     "kd_strerror": (ctypes.c_char_p, [_i]),
 }
@@ -57,7 +73,8 @@ for _name, (_res, _args) in _SIGS.items():
 
 D_C, D_R = 512, 64
 KD_DEV_BITS = {0x01: "BAD_PARENT", 0x02: "CACHE_FULL", 0x04: "BAD_PATH",
-               0x08: "BAD_POSITION", 0x10: "TIMEOUT", 0x20: "BAD_MASK", 0x40: "BAD_PAGE"}
+               0x08: "BAD_POSITION", 0x10: "TIMEOUT", 0x20: "BAD_MASK", 0x40: "BAD_PAGE",
+               0x80: "BAD_SEQLENS"}
 
 
 class KdError(RuntimeError):
@@ -361,6 +378,338 @@ def kd_kv_compact_paged(c_pages, r_pages, page_table, page_size, path, length, c
     _check(lib.kd_kv_compact_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table),
                                    M, N, _ptr(path), _ptr(length), _ptr(cache_lens), B, n,
                                    _ptr(dev_error), _stream(stream)), "kd_kv_compact_paged")
+
+
+# ------------------------------------------------------------------ operators next to the verify step
+def _on_device(*tensors):
+    """Every tensor given (None skipped) lies on the current CUDA device, whose stream runs the call."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"tensor on cuda:{t.device.index}, the current device is cuda:{dev}")
+
+
+def _typed(t, dtype, name, shape=None):
+    """Contiguous tensor of `dtype` and, when given, of `shape`."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
+
+
+def _heads(t, name, heads=None, width=None):
+    """Token and head strides of a bf16 [tokens][heads][width] view (unit stride inside a head)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.numel() and t.stride(2) != 1):
+        raise ValueError(f"{name} must be bf16 [tokens][heads][width], unit stride inside a head")
+    if (heads is not None and t.shape[1] != heads) or (width is not None and t.shape[2] != width):
+        raise ValueError(f"{name} must be [tokens][{heads}][{width}], is {tuple(t.shape)}")
+    if t.numel() == 0:
+        return 0, 0
+    return t.stride(0), t.stride(1)
+
+
+def _rope_table(table, rot):
+    _typed(table, torch.float32, "rope_table")
+    if table.dim() != 2 or (rot is not None and table.shape[1] != rot):
+        raise ValueError("rope_table must be [max_pos][rot]")
+    return table.shape[0], table.shape[1]
+
+
+def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, eps=1e-6, rot_offset=0,
+                    interleaved=False, q_out=None, k_out=None, dev_error=None, stream=None):
+    """RMS norm of every head of q [T][H][D] and k [T][Hk][D] (k None: queries alone; a weight
+    None: no norm) and the rotation of its elements [rot_offset, rot_offset + rot) by
+    positions [T] int32; rope_table fp32 [max_pos][rot], cos | sin.  Returns (q_out, k_out),
+    allocated contiguous unless given; q_out=q, k_out=k works in place."""
+    _on_device(q, k, positions, rope_table, q_weight, k_weight, q_out, k_out, dev_error)
+    qt, qh = _heads(q, "q")
+    T, H, D = q.shape
+    _typed(positions, torch.int32, "positions", (T,))
+    max_pos, rot = _rope_table(rope_table, None)
+    if q_weight is not None:
+        _typed(q_weight, torch.bfloat16, "q_weight", (D,))
+    if q_out is None:
+        q_out = torch.empty(T, H, D, dtype=torch.bfloat16, device=q.device)
+    elif q_out.shape[0] != T:
+        raise ValueError("q_out must have q's shape")
+    qot, qoh = _heads(q_out, "q_out", H, D)
+    Hk = kt = kh = kot = koh = 0
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 3 else 0
+        kt, kh = _heads(k, "k", Hk, D)
+        if k.shape[0] != T:
+            raise ValueError("q and k must have the same tokens")
+        if k_weight is not None:
+            _typed(k_weight, torch.bfloat16, "k_weight", (D,))
+        if k_out is None:
+            k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=q.device)
+        elif k_out.shape[0] != T:
+            raise ValueError("k_out must have k's shape")
+        kot, koh = _heads(k_out, "k_out", Hk, D)
+    _check(lib.kd_qk_norm_rope(_ptr(q), qt, qh, _ptr(k), kt, kh, _ptr(q_weight), _ptr(k_weight), eps,
+                               _ptr(rope_table), max_pos, _ptr(positions), T, H, Hk, D, rot, rot_offset,
+                               int(interleaved), _ptr(q_out), qot, qoh, _ptr(k_out), kot, koh, _ptr(dev_error),
+                               _stream(stream)), "kd_qk_norm_rope")
+    return q_out, k_out
+
+
+def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B, q_rope_in, q_rope_out):
+    _typed(cache_lens, torch.int32, "cache_lens")
+    if B is None:
+        B = cache_lens.shape[0]
+    if cache_lens.shape[0] != B:
+        raise ValueError("cache_lens must be [B]")
+    if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != D_C + D_R or (kv.numel() and kv.stride(1) != 1):
+        raise ValueError("kv must be bf16 [T][576] with unit-stride rows")
+    T = kv.shape[0]
+    max_pos, _ = _rope_table(rope_table, D_R)
+    if positions is not None:
+        _typed(positions, torch.int32, "positions", (T,))
+    if kv_weight is not None:
+        _typed(kv_weight, torch.bfloat16, "kv_weight", (D_C,))
+    if cu_seqlens is not None:
+        _typed(cu_seqlens, torch.int32, "cu_seqlens", (B + 1,))
+    elif T % B:
+        raise ValueError("without cu_seqlens the tokens must divide evenly among the requests")
+    H = qt = qh = 0
+    if q_rope_in is not None:
+        H = q_rope_in.shape[1] if q_rope_in.dim() == 3 else 0
+        qt, qh = _heads(q_rope_in, "q_rope_in", H, D_R)
+        if q_rope_in.shape[0] != T:
+            raise ValueError("q_rope_in must be [T][H][64]")
+        if q_rope_out is None:
+            q_rope_out = torch.empty(T, H, D_R, dtype=torch.bfloat16, device=kv.device)
+        _typed(q_rope_out, torch.bfloat16, "q_rope_out", (T, H, D_R))
+    elif q_rope_out is not None:
+        raise ValueError("q_rope_out without q_rope_in")
+    return B, T, max_pos, H, qt, qh, q_rope_out
+
+
+def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens=None, B=None,
+                          kv_weight=None, eps=1e-6, interleaved=True, q_rope_in=None, q_rope_out=None,
+                          dev_error=None, stream=None):
+    """Cache rows of new tokens from the down-projection's output kv [T][576]: the latent
+    normed, the rope key rotated, both stored at slots cache_lens[b] + i; the queries' rope
+    part q_rope_in [T][H][64] rotated beside them.  positions None: cache_lens[b] + i;
+    cu_seqlens None: T / B tokens per request.  Returns q_rope_out (None without queries)."""
+    _on_device(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in, q_rope_out,
+               dev_error)
+    sc, sr, cap = _cache_strides(c_kv, k_rope)
+    B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
+                                                       q_rope_in, q_rope_out)
+    if c_kv.shape[0] != B:
+        raise ValueError("the cache must hold B requests")
+    _check(lib.kd_kv_norm_rope_write(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(kv), kv.stride(0),
+                                     _ptr(kv_weight), eps, _ptr(rope_table), max_pos, _ptr(positions),
+                                     int(interleaved), _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H,
+                                     _ptr(q_rope_out), _ptr(dev_error), _stream(stream)), "kd_kv_norm_rope_write")
+    return q_rope_out
+
+
+def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_lens, kv, positions, rope_table,
+                                cu_seqlens=None, B=None, kv_weight=None, eps=1e-6, interleaved=True, q_rope_in=None,
+                                q_rope_out=None, dev_error=None, stream=None):
+    """kd_kv_norm_rope_write through a page table."""
+    _on_device(c_pages, r_pages, page_table, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in,
+               q_rope_out, dev_error)
+    sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
+    B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
+                                                       q_rope_in, q_rope_out)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pages per request]")
+    _check(lib.kd_kv_norm_rope_write_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
+                                           _ptr(cache_lens), _ptr(kv), kv.stride(0), _ptr(kv_weight), eps,
+                                           _ptr(rope_table), max_pos, _ptr(positions), int(interleaved),
+                                           _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H, _ptr(q_rope_out),
+                                           _ptr(dev_error), _stream(stream)), "kd_kv_norm_rope_write_paged")
+    return q_rope_out
+
+
+def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu_seqlens_k=None, scale=None, out=None,
+                   lse=None, dev_error=None, stream=None):
+    """Causal attention of packed prompts: q_nope [T][H][128], k_nope and v [Tk][Hk][128], and
+    with a rope part q_rope [T][H][64] and k_rope [Tk][Hk][64] (or [Tk][64]: one for all
+    heads), any token and head strides; sequence b is rows cu_seqlens_q[b] .. [b + 1] of the
+    queries and of the keys (cu_seqlens_k when those differ: the queries are the last
+    positions).  scale None: 1 / sqrt(192) with a rope part, else 1 / sqrt(128).
+    Returns (out [T][H][128] bf16, lse [T][H] fp32)."""
+    _on_device(q_nope, k_nope, v, cu_seqlens_q, q_rope, k_rope, cu_seqlens_k, out, lse, dev_error)
+    qnt, qnh = _heads(q_nope, "q_nope", None, 128)
+    T, H, _ = q_nope.shape
+    knt, knh = _heads(k_nope, "k_nope", None, 128)
+    Tk, Hk, _ = k_nope.shape
+    vt, vh = _heads(v, "v", Hk, 128)
+    if v.shape[0] != Tk:
+        raise ValueError("k_nope and v must have the same tokens")
+    if (q_rope is None) != (k_rope is None):
+        raise ValueError("q_rope and k_rope go together")
+    qrt = qrh = krt = krh = 0
+    if q_rope is not None:
+        qrt, qrh = _heads(q_rope, "q_rope", H, D_R)
+        if k_rope.dim() == 2:
+            krt, krh = _heads(k_rope.unsqueeze(1), "k_rope", 1, D_R)[0], 0
+        else:
+            krt, krh = _heads(k_rope, "k_rope", Hk, D_R)
+        if q_rope.shape[0] != T or k_rope.shape[0] != Tk:
+            raise ValueError("q_rope and k_rope must have q_nope's and k_nope's tokens")
+    _typed(cu_seqlens_q, torch.int32, "cu_seqlens_q")
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
+        raise ValueError("cu_seqlens_q must be [B + 1]")
+    B = cu_seqlens_q.shape[0] - 1
+    if cu_seqlens_k is not None:
+        _typed(cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(128.0 if q_rope is None else 192.0)
+    if out is None:
+        out = torch.empty(T, H, 128, dtype=torch.bfloat16, device=q_nope.device)
+    if lse is None:
+        lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
+    _typed(out, torch.bfloat16, "out", (T, H, 128))
+    _typed(lse, torch.float32, "lse", (T, H))
+    _check(lib.kd_prompt_attn(_ptr(q_nope), qnt, qnh, _ptr(q_rope), qrt, qrh, _ptr(k_nope), knt, knh, _ptr(k_rope),
+                              krt, krh, _ptr(v), vt, vh, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, T, Tk, H, Hk,
+                              scale, _ptr(out), _ptr(lse), _ptr(dev_error), _stream(stream)), "kd_prompt_attn")
+    return out, lse
+
+
+def _weight_rows(w, B, cap, name):
+    if w.dtype != torch.float32 or w.dim() != 2 or w.shape[0] != B or w.shape[1] < cap or w.stride(1) != 1:
+        raise ValueError(f"{name} must be fp32 [{B}][at least {cap}] with unit-stride rows")
+    return w.stride(0) if B > 1 else max(w.stride(0), w.shape[1])
+
+
+def _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, cap):
+    _typed(q_abs, torch.bfloat16, "q_abs")
+    if q_abs.dim() != 4 or q_abs.shape[3] != D_C:
+        raise ValueError("q_abs must be [B][n][H][512]")
+    B, n, H, _ = q_abs.shape
+    _typed(q_rope, torch.bfloat16, "q_rope", (B, n, H, D_R))
+    _typed(cache_lens, torch.int32, "cache_lens", (B,))
+    _need(vis, (torch.int32, torch.uint32), "vis")
+    if tuple(vis.shape) != (B, n, (n + 31) // 32):
+        raise ValueError("vis must be [B][n][ceil(n / 32)]")
+    _typed(lse, torch.float32, "lse", (B, n, H))
+    if (path is None) != (length is None):
+        raise ValueError("path and length go together")
+    if path is not None:
+        _typed(path, torch.int32, "path", (B, n))
+        _typed(length, torch.int32, "length", (B,))
+    if weights_out is None:
+        weights_out = torch.zeros(B, cap, dtype=torch.float32, device=q_abs.device)
+    wi = _weight_rows(weights_in, B, cap, "weights_in") if weights_in is not None else 0
+    return B, n, H, wi, _weight_rows(weights_out, B, cap, "weights_out"), weights_out
+
+
+def kd_kv_attn_weights(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path=None, length=None,
+                       scale=1.0 / math.sqrt(192.0), weights_in=None, weights_out=None, dev_error=None, stream=None):
+    """Attention weight each cache slot receives from the accepted nodes (path, length of
+    kd_tree_accept; None: every node), added to weights_in [B][>= cap] fp32 (None: zeros).
+    lse is kd_tree_verify_attn's.  Call it before kd_kv_compact: the new slots' weights are
+    stored in compacted order.  Returns weights_out (weights_out=weights_in accumulates)."""
+    _on_device(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, dev_error)
+    sc, sr, cap = _cache_strides(c_kv, k_rope)
+    B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
+                                                 weights_out, cap)
+    if c_kv.shape[0] != B:
+        raise ValueError("the cache must hold B requests")
+    _check(lib.kd_kv_attn_weights(_ptr(q_abs), _ptr(q_rope), _ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens),
+                                  _ptr(vis), _ptr(lse), _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
+                                  _ptr(weights_out), wo, _ptr(dev_error), _stream(stream)), "kd_kv_attn_weights")
+    return weights_out
+
+
+def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_size, cache_lens, vis, lse, path=None,
+                             length=None, scale=1.0 / math.sqrt(192.0), weights_in=None, weights_out=None,
+                             dev_error=None, stream=None):
+    """kd_kv_attn_weights over a paged cache (page_size 64, 128 or 256)."""
+    _on_device(q_abs, q_rope, c_pages, r_pages, page_table, cache_lens, vis, lse, path, length, weights_in,
+               weights_out, dev_error)
+    sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
+    B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
+                                                 weights_out, M * page_size)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pages per request]")
+    _check(lib.kd_kv_attn_weights_paged(_ptr(q_abs), _ptr(q_rope), _ptr(c_pages), _ptr(r_pages), sc, sr,
+                                        int(page_size), _ptr(page_table), M, N, _ptr(cache_lens), _ptr(vis), _ptr(lse),
+                                        _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
+                                        _ptr(weights_out), wo, _ptr(dev_error), _stream(stream)),
+           "kd_kv_attn_weights_paged")
+    return weights_out
+
+
+def _evict_args(cache_lens, weights_in, cap, dst_cap, keep, inplace, weights_out, lens_out, kept):
+    _typed(cache_lens, torch.int32, "cache_lens")
+    B, dev = cache_lens.shape[0], cache_lens.device
+    wi = _weight_rows(weights_in, B, cap, "weights_in")
+    rows = min(dst_cap, max(int(keep), 1))
+    if weights_out is None:
+        weights_out = weights_in if inplace else torch.zeros(B, dst_cap, dtype=torch.float32, device=dev)
+    wo = _weight_rows(weights_out, B, rows, "weights_out")
+    if lens_out is None:
+        lens_out = cache_lens if inplace else torch.empty(B, dtype=torch.int32, device=dev)
+    _typed(lens_out, torch.int32, "lens_out", (B,))
+    if kept is None:
+        kept = torch.empty(B, max(int(keep), 1), dtype=torch.int32, device=dev)
+    _typed(kept, torch.int32, "kept", (B, max(int(keep), 1)))
+    return B, wi, wo, weights_out, lens_out, kept
+
+
+def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_dst=None, r_dst=None,
+                weights_out=None, lens_out=None, kept=None, dev_error=None, stream=None):
+    """Cuts every request's cache to at most `keep` slots: its first `sink`, its last `recent`
+    and those of the largest weights between.  Without c_dst, r_dst it works in place (cache,
+    cache_lens and weights_in are updated); with them the kept rows go to another cache.
+    Returns (kept [B][keep] int32, weights_out, lens_out)."""
+    _on_device(c_kv, k_rope, cache_lens, weights_in, c_dst, r_dst, weights_out, lens_out, kept, dev_error)
+    sc, sr, cap = _cache_strides(c_kv, k_rope)
+    if (c_dst is None) != (r_dst is None):
+        raise ValueError("c_dst and r_dst go together")
+    inplace = c_dst is None
+    if inplace:
+        c_dst, r_dst = c_kv, k_rope
+    dc, dr, dcap = _cache_strides(c_dst, r_dst)
+    B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, cap, dcap, keep, inplace, weights_out,
+                                                         lens_out, kept)
+    if c_kv.shape[0] != B or c_dst.shape[0] != B:
+        raise ValueError("the caches must hold B requests")
+    _check(lib.kd_kv_evict(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(weights_in), wi, int(keep),
+                           int(sink), int(recent), B, _ptr(c_dst), _ptr(r_dst), dc, dr, dcap, _ptr(weights_out), wo,
+                           _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream(stream)), "kd_kv_evict")
+    return kept, weights_out, lens_out
+
+
+def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weights_in, keep, sink=0, recent=0,
+                      c_dst=None, r_dst=None, dst_page_table=None, weights_out=None, lens_out=None, kept=None,
+                      dev_error=None, stream=None):
+    """kd_kv_evict through page tables: in place without dst_page_table (the request's tail
+    pages are then free), else into the pages of dst_page_table (of c_dst, r_dst, or of the
+    same pool), which must be none of the source's."""
+    _on_device(c_pages, r_pages, page_table, cache_lens, weights_in, c_dst, r_dst, dst_page_table, weights_out,
+               lens_out, kept, dev_error)
+    sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
+    if (c_dst is None) != (r_dst is None) or (c_dst is not None and dst_page_table is None):
+        raise ValueError("c_dst, r_dst and dst_page_table go together")
+    inplace = dst_page_table is None
+    if inplace:
+        dst_page_table = page_table
+    if c_dst is None:
+        c_dst, r_dst = c_pages, r_pages
+    dc, dr, DM, DN = _page_args(c_dst, r_dst, dst_page_table, page_size)
+    B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, M * page_size, DM * page_size, keep,
+                                                         inplace, weights_out, lens_out, kept)
+    if page_table.shape[0] != B or dst_page_table.shape[0] != B:
+        raise ValueError("page tables must be [B][pages per request]")
+    _check(lib.kd_kv_evict_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
+                                 _ptr(cache_lens), _ptr(weights_in), wi, int(keep), int(sink), int(recent), B,
+                                 _ptr(c_dst), _ptr(r_dst), dc, dr, _ptr(dst_page_table), DM, DN, _ptr(weights_out), wo,
+                                 _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream(stream)), "kd_kv_evict_paged")
+    return kept, weights_out, lens_out
 
 
 def kd_read_device_error(word, clear=True, stream=None) -> int:
