@@ -1,73 +1,477 @@
-// Attention weight that each cache slot receives from the counted nodes, one warp per
-// slot: every counted node and head in turn, the dot product split over the lanes.
+// Attention weight that each cache slot receives from the counted nodes (tcgen05 + TMEM +
+// TMA):
+//   col_j = sum over counted rows (node i, head h) that see slot j of exp(s_ihj - lse_ih).
+//
+// The scores are computed transposed, S^T = K Q^T: 128 keys are the M rows of the MMA (the
+// TMEM lanes), up to 256 query rows its N columns.  A thread of the epilogue then owns one
+// key and adds up along its own columns: no reduction between threads, no second product,
+// a fixed order.  With the rows' lse known, one pass is enough: nothing runs a maximum.
+//
+// A unit is (request, 128 keys); a cluster of 1, 2, 4 or 8 CTAs shares a unit by dealing
+// the query tiles out among its CTAs, whose sums meet in the first CTA's shared memory.
+// Per CTA, K (128 keys x 576, nine 16 KB chunks of 64 columns) stays in shared memory for
+// the unit; Q streams past it from L2 through a ring of 32 KB stages (256 rows x 64
+// columns).  A K chunk is refilled for the next unit as soon as the last query tile has
+// used it, so that with few rows (one query tile: bound by the cache's bytes) the next
+// unit's keys stream in behind the current one's products.
+//
+// Query tiles hold whole nodes: rows of one node are contiguous in memory, nodes on an
+// accepted path are not, so a stage is filled by one box per node, 16-row aligned (rows
+// that pad a node up are zeroed once and get lse = inf).  When every node counts and H is a
+// multiple of 16, one box fills the stage.
+//
+// Roles: warp 0 loads K, warp 1 loads Q, warp 2 issues the MMAs, warp 3 stages the rows'
+// lse and masks, warps 4 to 11 are the epilogue (two groups of four warps, taking the S
+// tile's 32-column chunks in turn).  Two S tiles of 256 TMEM columns alternate.  Every wait
+// is bounded (kd_pipe.cuh).  No TMA multicast.
+
 #include <math.h>
 
-#include "kd_common.cuh"
-#include "kd_ptx.cuh"
+#include <atomic>
+
+#include "kd_pipe.cuh"
 #include "kd_slots.cuh"
+#include "kd_tmap.cuh"
 
 namespace kd {
 namespace aw {
 
+using namespace ptx;
+
+constexpr int THREADS = 384;
+constexpr int BK = 128;                       // keys per unit
+constexpr int BN = 256;                       // query rows per tile
+constexpr int NCH = 9;                        // 64-column chunks: 8 latent, 1 rope
+constexpr int KCHUNK = BK * 128;              // bytes
+constexpr int QSTAGE = BN * 128;
+constexpr int NQ = 2;                         // Q ring stages
+constexpr int NS = 2;                         // S tiles in TMEM
+constexpr int MAXC = 8;                       // CTAs of a cluster
+
+enum Bar {
+  K_FULL = 0,                   // chunk landed (TMA)
+  K_FREE = K_FULL + NCH,        // chunk used for the last time in its unit (MMA commit)
+  Q_FULL = K_FREE + NCH,
+  Q_FREE = Q_FULL + NQ,
+  Z_FULL = Q_FREE + NQ,         // lse and masks of the tile staged (32 arrivals)
+  S_FULL = Z_FULL + NS,
+  S_FREE = S_FULL + NS,         // S tile and its lse read (256 arrivals)
+  P_FULL = S_FREE + NS,         // first CTA: the others' sums of a unit arrived
+  P_FREE = P_FULL + 2,          // other CTAs: the first has read them
+  DRAIN = P_FREE + 2,           // all MMAs done
+  NBAR = DRAIN + 1
+};
+constexpr int OFF_ABORT = 512, OFF_TMEM = 516;
+constexpr int OFF_Z = 1024;                             // f32 [NS][256]: -lse log2(e), -inf for a row that adds nothing
+constexpr int OFF_NODE = OFF_Z + NS * BN * 4;           // u8 [NS][256]: node of each column
+constexpr int OFF_VIS = OFF_NODE + NS * BN;             // u32 [NS][128][4]: masks of the tile's nodes, by place in the tile
+constexpr int OFF_X = OFF_VIS + NS * 128 * 16;          // f32 [2][128]: sums of the second group
+constexpr int OFF_PART = OFF_X + 2 * BK * 4;            // f32 [2][MAXC - 1][128]: sums of the other CTAs
+constexpr int OFF_K = ((OFF_PART + 2 * (MAXC - 1) * BK * 4 + 1023) / 1024) * 1024;
+constexpr int OFF_Q = OFF_K + NCH * KCHUNK;
+constexpr int SMEM = OFF_Q + NQ * QSTAGE + 1024;
+static_assert(NBAR * 8 <= OFF_ABORT && SMEM <= 232448, "shared memory");
+
 struct Params {
-  const uint16_t *qa, *qr, *c, *r;
-  int64_t sc, sr;
-  SlotMap map;
-  const int32_t *lens, *path, *len;
+  const int32_t *lens, *path, *len, *pt;
   const uint32_t* vis;
   const float *lse, *w_in;
   float* w_out;
-  int64_t wi, wo;
   int32_t* err;
-  int B, n, H, W;
-  float scale;
+  int64_t cap, wi, wo, pages;
+  int B, n, H, W, P, M;         // page size (0: contiguous) and pages per request
+  int Hp, per_tile;             // rows a node takes in a tile, nodes per tile
+  int linear;                   // one box per stage: `linear` rows (0: a box per node)
+  int kbox;                     // rows of a K box
+  float scale_log2;
 };
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-
-__global__ void __launch_bounds__(256) weights_kernel(const Params p) {
-  __shared__ int nodes[KD_MAX_NODES];
-  __shared__ int bad;
-  const int b = blockIdx.y, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int64_t L = p.lens[b];
-  const int count = p.path ? p.len[b] : p.n;
-  if (tid == 0) bad = L < 0 || L + p.n > p.map.cap ? KD_DEV_CACHE_FULL : (count < 1 || count > p.n) ? KD_DEV_BAD_PATH : 0;
-  __syncthreads();
-  if (!bad) {
-    if (tid < count) {
-      const int k = p.path ? p.path[(size_t)b * p.n + tid] : tid;
-      nodes[tid] = k;
-      if (k < 0 || k >= p.n) atomicOr(&bad, KD_DEV_BAD_PATH);
+// Cursor over the units of this cluster: units are numbered request by request, cluster c
+// takes c, c + clusters, ...  A warp looks at 32 requests at once.
+struct Cursor {
+  int b, kt;                    // current unit
+  int64_t L;
+  int count, tiles;             // counted nodes, query tiles
+  int base, b0, incl, step, u;  // window of 32 requests: first request, units before it, inclusive sums
+  __device__ __forceinline__ static int units_of(const Params& p, int b) {
+    if (b >= p.B) return 0;
+    const int64_t L = p.lens[b];
+    if (L < 0 || L + p.n > p.cap) return 1;             // one unit that reports it
+    const int c = p.path ? p.len[b] : p.n;
+    if (c < 1 || c > p.n) return 1;
+    return (int)((L + p.n + BK - 1) / BK);
+  }
+  __device__ __forceinline__ void window(const Params& p, int first) {
+    b0 = first;
+    incl = units_of(p, b0 + (threadIdx.x & 31));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if ((int)(threadIdx.x & 31) >= d) incl += o;
     }
-    if (p.map.pt)
-      for (int64_t q = tid; q * p.map.P < L + p.n; q += 256)
-        if (!p.map.pages_ok(b, q * p.map.P, q * p.map.P + 1)) atomicOr(&bad, KD_DEV_BAD_PAGE);
   }
+  __device__ __forceinline__ void start(const Params& p, int cluster, int clusters) {
+    base = 0;
+    u = cluster - clusters;
+    step = clusters;
+    window(p, 0);
+  }
+  // The next unit; false when there is none.  `bad`: KD_DEV_* bits of a request that has no work.
+  __device__ __forceinline__ bool next(const Params& p, int& bad) {
+    u += step;
+    int total = __shfl_sync(0xffffffffu, incl, 31);
+    while (u - base >= total) {
+      base += total;
+      if (b0 + 32 >= p.B) return false;
+      window(p, b0 + 32);
+      total = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int at = u - base;
+    const unsigned past = __ballot_sync(0xffffffffu, incl <= at);
+    const int i = __popc(past);
+    b = b0 + i;
+    const int before = __shfl_sync(0xffffffffu, incl, i ? i - 1 : 0);
+    kt = at - (i ? before : 0);
+    L = p.lens[b];
+    bad = 0;
+    count = p.path ? p.len[b] : p.n;
+    if (L < 0 || L + p.n > p.cap) bad = KD_DEV_CACHE_FULL;
+    else if (count < 1 || count > p.n) bad = KD_DEV_BAD_PATH;
+    tiles = bad ? 0 : (count + p.per_tile - 1) / p.per_tile;
+    return true;
+  }
+};
+
+// Node of place m on the path, kept inside [0, n) (a bad path is reported by the epilogue).
+__device__ __forceinline__ int node_at(const Params& p, int b, int m) {
+  if (!p.path) return m;
+  const int k = p.path[(size_t)b * p.n + m];
+  return k < 0 || k >= p.n ? 0 : k;
+}
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t saddr) { return smem_desc_sw128(saddr, 16, 1024); }
+
+// (d0, d1) = (a0, a1) * s + (c0, c1)
+__device__ __forceinline__ void ffma2v(float& d0, float& d1, float a0, float a1, float s, float c0, float c1) {
+  asm("{\n\t.reg .b64 ra, rs, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
+      "fma.rn.f32x2 rd, ra, rs, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(s), "f"(c0), "f"(c1));
+}
+
+// Adds exp2(s * scale + z) of four columns.
+__device__ __forceinline__ void add4(float (&acc)[4], const uint32_t* s, const float4& z, float scale) {
+  float a, b, c, d;
+  ffma2v(a, b, __uint_as_float(s[0]), __uint_as_float(s[1]), scale, z.x, z.y);
+  ffma2v(c, d, __uint_as_float(s[2]), __uint_as_float(s[3]), scale, z.z, z.w);
+  fadd2(acc[0], acc[1], ex2(a), ex2(b));
+  fadd2(acc[2], acc[3], ex2(c), ex2(d));
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant__ CUtensorMap tm_qr,
+               const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_r, const Params p,
+               const int csize) {
+  extern __shared__ uint8_t dyn[];
+  uint8_t* gbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+  const uint32_t base = smem_u32(gbase);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = csize > 1 ? (int)cluster_ctarank() : 0;
+  const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
+  const Pipe pipe{base, abort_flag, p.err};
+
+  // the rows that pad a node stay zero: no box ever writes them
+  for (int i = threadIdx.x; i < NQ * QSTAGE / 16; i += THREADS)
+    reinterpret_cast<uint4*>(gbase + OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    for (int i = 0; i < NBAR; ++i) {
+      const bool z = i >= Z_FULL && i < Z_FULL + NS, s = i >= S_FREE && i < S_FREE + NS;
+      const bool pf = i >= P_FULL && i < P_FULL + 2;
+      mbar_init(base + 8 * i, z ? 32 : s ? 256 : pf ? (csize > 1 ? 128 * (csize - 1) : 1) : 1);
+    }
+    fence_mbar_init();
+  }
+  fence_proxy_async_cta();
+  if (warp == 3) {
+    tmem_alloc(base + OFF_TMEM, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_qa);
+    tma_prefetch_desc(&tm_qr);
+    tma_prefetch_desc(&tm_c);
+    tma_prefetch_desc(&tm_r);
+  }
+  tc_fence_before();
   __syncthreads();
-  if (bad) {
-    if (tid == 0 && blockIdx.x == 0) raise_dev_error(p.err, bad);
-    return;
-  }
-  // slots [0, L), then the counted nodes' slots in path order
-  for (int64_t w = blockIdx.x * 8 + (tid >> 5); w < L + count; w += (int64_t)gridDim.x * 8) {
-    const int node = w < L ? -1 : nodes[w - L];
-    const int64_t row = p.map.row(b, w < L ? w : L + node);
-    float c[16], r[2], sum = 0.f;
-    for (int e = 0; e < 16; ++e) c[e] = bf(p.c[row * p.sc + e * 32 + lane]);
-    for (int e = 0; e < 2; ++e) r[e] = bf(p.r[row * p.sr + e * 32 + lane]);
-    for (int m = 0; m < count; ++m) {
-      const int64_t i = (int64_t)b * p.n + nodes[m];
-      if (node >= 0 && !(p.vis[i * p.W + (node >> 5)] >> (node & 31) & 1u)) continue;
-      for (int h = 0; h < p.H; ++h) {
-        const float z = p.lse[i * p.H + h];
-        float s = 0.f;
-        for (int e = 0; e < 16; ++e) s += c[e] * bf(p.qa[(i * p.H + h) * KD_D_C + e * 32 + lane]);
-        for (int e = 0; e < 2; ++e) s += r[e] * bf(p.qr[(i * p.H + h) * KD_D_R + e * 32 + lane]);
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (z != -INFINITY) sum += expf(s * p.scale - z);
+  if (csize > 1) cluster_sync();                        // barriers of all CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM);
+
+  Cursor cur;
+  int bad;
+  if (warp < 4) cur.start(p, cluster, clusters);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K
+    uint32_t it = 0;                                    // units loaded
+    bool ok = true;
+    while (ok && cur.next(p, bad)) {
+      if (bad || rank >= cur.tiles) continue;
+      int64_t row[2];
+      const int boxes = BK / p.kbox;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t key = (int64_t)cur.kt * BK + i * p.kbox;
+        if (!p.P) row[i] = (int64_t)cur.b * p.cap + key;
+        else {
+          const int64_t q = key / p.P;                  // pages past the last one, or bad ones: page 0
+          const int32_t id = q < p.M ? p.pt[(size_t)cur.b * p.M + q] : 0;
+          row[i] = (id < 0 || id >= p.pages ? 0 : (int64_t)id * p.P) + key % p.P;
+        }
+      }
+      int c = 0;
+      for (; c < NCH; ++c) {
+        if (!(ok = pipe.wait_warp(K_FREE + c, (it & 1u) ^ 1u))) break;
+        if (lane == 0) {
+          const uint32_t bar = pipe.bar(K_FULL + c);
+          mbar_arrive_expect_tx(bar, KCHUNK);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_3d(base + OFF_K + c * KCHUNK + i * p.kbox * 128, c < 8 ? &tm_c : &tm_r, c < 8 ? c * 64 : 0,
+                        (int32_t)row[i], 0, bar);
+        }
+        __syncwarp();
+      }
+      if (ok) ++it;
+      else
+        while (c-- > 0) pipe.drain(K_FULL + c, it & 1u);  // chunks of this unit that were asked for
+    }
+    if (it > 0)
+      for (int c = 0; c < NCH; ++c) pipe.drain(K_FULL + c, (it - 1) & 1u);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ Q
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && cur.next(p, bad)) {
+      if (bad) continue;
+      for (int t = rank; t < cur.tiles && ok; t += csize) {
+        const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0);
+        // lane i loads the box of node m0 + i (+ 32, ...): rows of the flat [B n H] query
+        for (int c = 0; c < NCH && ok; ++c, ++it) {
+          const uint32_t st = it % NQ;
+          if (!(ok = pipe.wait_warp(Q_FREE + st, ((it / NQ) & 1u) ^ 1u))) break;
+          const uint32_t bar = pipe.bar(Q_FULL + st), dst = base + OFF_Q + st * QSTAGE;
+          const CUtensorMap* map = c < 8 ? &tm_qa : &tm_qr;
+          const int x = c < 8 ? c * 64 : 0;
+          if (lane == 0) mbar_arrive_expect_tx(bar, (p.linear ? p.linear : nodes * p.H) * 128);
+          __syncwarp();
+          if (p.linear) {
+            if (lane == 0) tma_load_3d(dst, map, x, ((int64_t)cur.b * p.n + m0) * p.H, 0, bar);
+          } else {
+            for (int i = lane; i < nodes; i += 32)
+              tma_load_3d(dst + i * p.Hp * 128, map, x, (cur.b * p.n + node_at(p, cur.b, m0 + i)) * p.H, 0, bar);
+          }
+          __syncwarp();
+        }
       }
     }
-    if (lane == 0) p.w_out[b * p.wo + w] = sum + (w < L && p.w_in ? p.w_in[b * p.wi + w] : 0.f);
+    for (uint32_t j = it > NQ ? it - NQ : 0; j < it; ++j) pipe.drain(Q_FULL + j % NQ, (j / NQ) & 1u);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ MMA
+    uint32_t it = 0, ts = 0, un = 0;
+    bool ok = true;
+    while (ok && cur.next(p, bad)) {
+      if (bad || rank >= cur.tiles) continue;
+      for (int t = rank; t < cur.tiles && ok; t += csize, ++ts) {
+        const int nodes = min(p.per_tile, cur.count - t * p.per_tile);
+        const uint32_t idesc = idesc_bf16(BK, nodes * p.Hp, 0, 0);
+        const uint32_t sb = ts % NS, d = tmem + sb * BN;
+        const bool first = t == rank, last = t + csize >= cur.tiles;
+        if (!(ok = pipe.wait_warp(S_FREE + sb, ((ts / NS) & 1u) ^ 1u))) break;
+        tc_fence_after();
+        for (int c = 0; c < NCH; ++c, ++it) {
+          const uint32_t st = it % NQ;
+          if (first && !(ok = pipe.wait_warp(K_FULL + c, un & 1u))) break;
+          if (!(ok = pipe.wait_warp(Q_FULL + st, (it / NQ) & 1u))) break;
+          if (lane == 0) {
+            const uint64_t a = desc_of(base + OFF_K + c * KCHUNK), b = desc_of(base + OFF_Q + st * QSTAGE);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_bf16_ss(d, a + 2 * k, b + 2 * k, idesc, c + k > 0);
+            tc_commit(pipe.bar(Q_FREE + st));
+            if (last) tc_commit(pipe.bar(K_FREE + c));
+          }
+          __syncwarp();
+        }
+        if (ok && lane == 0) tc_commit(pipe.bar(S_FULL + sb));
+        __syncwarp();
+      }
+      ++un;
+    }
+    if (lane == 0) tc_commit(pipe.bar(DRAIN));
+    __syncwarp();
+    pipe.drain(DRAIN, 0);                               // no MMA in flight when TMEM is released
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ lse and masks
+    uint32_t ts = 0;
+    bool ok = true;
+    while (ok && cur.next(p, bad)) {
+      if (bad) continue;
+      const bool tail = (int64_t)(cur.kt + 1) * BK > cur.L;
+      for (int t = rank; t < cur.tiles; t += csize, ++ts) {
+        const uint32_t sb = ts % NS;
+        if (!(ok = pipe.wait_warp(S_FREE + sb, ((ts / NS) & 1u) ^ 1u))) break;
+        float* z = reinterpret_cast<float*>(gbase + OFF_Z) + sb * BN;
+        uint8_t* col = gbase + OFF_NODE + sb * BN;
+        uint32_t* vis = reinterpret_cast<uint32_t*>(gbase + OFF_VIS) + sb * 128 * 4;
+        const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0);
+#pragma unroll
+        for (int j = lane; j < BN; j += 32) {
+          const int i = j / p.Hp, h = j - i * p.Hp;
+          float v = -INFINITY;
+          if (i < nodes && h < p.H) {
+            const float l = p.lse[((int64_t)cur.b * p.n + node_at(p, cur.b, m0 + i)) * p.H + h];
+            v = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+          }
+          z[j] = v;
+          if (tail) col[j] = (uint8_t)(i < nodes ? i : 0);
+        }
+        if (tail)
+          for (int i = lane; i < nodes; i += 32) {
+            const uint32_t* row = p.vis + ((size_t)cur.b * p.n + node_at(p, cur.b, m0 + i)) * p.W;
+            for (int w = 0; w < 4; ++w) vis[i * 4 + w] = w < p.W ? row[w] : 0u;
+          }
+        mbar_arrive(pipe.bar(Z_FULL + sb));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int tid = threadIdx.x - 128, g = tid >> 7, r = tid & 127;       // group, key of the unit
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t ts = 0, un = 0;
+    bool ok = true;
+    cur.start(p, cluster, clusters);
+    while (cur.next(p, bad)) {
+      if (bad) {
+        if (tid == 0 && rank == 0) raise_dev_error(p.err, bad);
+        continue;
+      }
+      // every CTA's view of the request: the same answer in all of them
+      bool out = false;
+      if (p.path && r < cur.count) {
+        const int k = p.path[(size_t)cur.b * p.n + r];
+        out = k < 0 || k >= p.n;
+        if (out) raise_dev_error(p.err, KD_DEV_BAD_PATH);
+      }
+      if (p.P)
+        for (int64_t q = tid; q * p.P < cur.L + p.n; q += 256) {
+          const int32_t id = p.pt[(size_t)cur.b * p.M + q];
+          if (id < 0 || id >= p.pages) {
+            out = true;
+            raise_dev_error(p.err, KD_DEV_BAD_PAGE);
+          }
+        }
+      out = named_bar_red_or(1, 256, out);
+      // a group that gave up at the end of the last unit takes the other one with it
+      if (csize > 1 && named_bar_red_or(1, 256, !ok)) break;
+      const int64_t key = (int64_t)cur.kt * BK + r;
+      const int k = key < cur.L ? -1 : (int)(key - cur.L);                // node of a tree slot
+      const bool tail = (int64_t)(cur.kt + 1) * BK > cur.L;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int t = rank; t < cur.tiles; t += csize, ++ts) {
+        const uint32_t sb = ts % NS, par = (ts / NS) & 1u;
+        const int rows = min(p.per_tile, cur.count - t * p.per_tile) * p.Hp;
+        ok = pipe.wait(Z_FULL + sb, par) && pipe.wait(S_FULL + sb, par);
+        if (named_bar_red_or(1, 256, !ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float* z = reinterpret_cast<const float*>(gbase + OFF_Z) + sb * BN;
+        const uint32_t src = tmem + lanes + sb * BN;
+        if (!tail) {
+          int j = g * 32;
+          for (; j + 32 <= rows; j += 64) {
+            uint32_t s[32];
+            tmem_ld32(src + j, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) add4(acc, s + i, *reinterpret_cast<const float4*>(z + j + i), p.scale_log2);
+          }
+          if (j < rows) {                               // 16 columns are left
+            uint32_t s[16];
+            tmem_ld16(src + j, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) add4(acc, s + i, *reinterpret_cast<const float4*>(z + j + i), p.scale_log2);
+          }
+        } else {
+          const uint8_t* col = gbase + OFF_NODE + sb * BN;
+          const uint32_t* vis = reinterpret_cast<const uint32_t*>(gbase + OFF_VIS) + sb * 128 * 4;
+          for (int j = g * 32; j < rows; j += 64)
+            for (int q = 0; q < 32 && j + q < rows; q += 16) {
+              uint32_t s[16];
+              tmem_ld16(src + j + q, s);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int jj = j + q + i;
+                const bool see = k < 0 || (k < p.n && (vis[col[jj] * 4 + (k >> 5)] >> (k & 31) & 1u));
+                const float e = ex2(__uint_as_float(s[i]) * p.scale_log2 + z[jj]);
+                acc[i & 3] += see ? e : 0.f;
+              }
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(pipe.bar(S_FREE + sb));
+      }
+      if (!ok) break;
+      // the two groups' sums, then the other CTAs' in rank order
+      float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      float* x = reinterpret_cast<float*>(gbase + OFF_X) + (un & 1) * BK;
+      if (g == 1) x[r] = sum;
+      named_bar_sync(1, 256);
+      const uint32_t slot = un & 1, turn = (un >> 1) & 1u;
+      ++un;
+      if (g == 0) {
+        sum += x[r];
+        if (csize > 1 && rank > 0) {
+          if (!(ok = __all_sync(0xffffffffu, pipe.wait_remote(P_FREE + slot, turn ^ 1u)))) continue;
+          const uint32_t to = map_to_rank(base + OFF_PART + ((slot * (MAXC - 1) + rank - 1) * BK + r) * 4, 0);
+          st_cluster_u32(to, __float_as_uint(sum));
+          mbar_arrive_remote(map_to_rank(pipe.bar(P_FULL + slot), 0));
+        } else {
+          if (csize > 1) {
+            if (!(ok = __all_sync(0xffffffffu, pipe.wait_remote(P_FULL + slot, turn)))) continue;
+            const float* part = reinterpret_cast<const float*>(gbase + OFF_PART) + slot * (MAXC - 1) * BK;
+            for (int i = 0; i < csize - 1; ++i) sum += part[i * BK + r];
+          }
+          if (!out) {
+            float* wo = p.w_out + (int64_t)cur.b * p.wo;
+            if (k < 0) wo[key] = sum + (p.w_in ? p.w_in[(int64_t)cur.b * p.wi + key] : 0.f);
+            else if (k < p.n) {
+              if (!p.path) wo[key] = sum;
+              else
+                for (int m = 0; m < cur.count; ++m)
+                  if (p.path[(size_t)cur.b * p.n + m] == k) wo[cur.L + m] = sum;
+            }
+          }
+          if (csize > 1) {
+            named_bar_sync(2, 128);                     // everyone has read the parts
+            if (r < csize - 1) mbar_arrive_remote(map_to_rank(pipe.bar(P_FREE + slot), r + 1));
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (csize > 1) cluster_sync();                        // no CTA leaves while another writes to it
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -76,23 +480,117 @@ __global__ void __launch_bounds__(256) weights_kernel(const Params p) {
 
 using namespace kd;
 
+// Clusters of `c` CTAs that fit on the device at once (cached per device).
+static int active_clusters(int c, int sms) {
+  static std::atomic<int> cached[64][4];
+  int dev = 0;
+  const int slot = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms / c;
+  int v = cached[dev][slot].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sms / c * c));
+  cfg.blockDim = dim3(aw::THREADS);
+  cfg.dynamicSmemBytes = aw::SMEM;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)c;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int nc = 0;
+  v = sms / c;
+  if (cudaOccupancyMaxActiveClusters(&nc, aw::weights_kernel, &cfg) == cudaSuccess && nc > 0) v = nc;
+  cudaGetLastError();
+  cached[dev][slot].store(v, std::memory_order_relaxed);
+  return v;
+}
+
 static int weights_impl(const kd_bf16_t* qa, const kd_bf16_t* qr, const kd_bf16_t* c, const kd_bf16_t* r, int64_t sc,
-                        int64_t sr, const SlotMap& map, int64_t cache_rows, const int32_t* lens, const uint32_t* vis,
-                        const float* lse, const int32_t* path, const int32_t* len, int B, int n, int H, float scale,
-                        const float* w_in, int64_t wi, float* w_out, int64_t wo, int32_t* dev_error,
-                        cudaStream_t stream) {
+                        int64_t sr, int64_t cap, int64_t cache_rows, const int32_t* pt, int page, int64_t M,
+                        int64_t pages, const int32_t* lens, const uint32_t* vis, const float* lse, const int32_t* path,
+                        const int32_t* len, int B, int n, int H, float scale, const float* w_in, int64_t wi,
+                        float* w_out, int64_t wo, int32_t* dev_error, cudaStream_t stream) {
   if (!qa || !qr || !lens || !vis || !lse || !w_out || !shapes_ok(B, n) || B > 65535 || H < 1 || H > KD_MAX_HEADS ||
-      !cache_ok(c, r, sc, sr, map.cap) || !aligned16(qa) || !aligned16(qr) || !(scale > 0.f && isfinite(scale)) ||
-      (path != nullptr) != (len != nullptr) || wo < map.cap || (w_in && wi < map.cap) || (w_in == w_out && wi != wo) ||
+      !cache_ok(c, r, sc, sr, cap) || !aligned16(qa) || !aligned16(qr) || !(scale > 0.f && isfinite(scale)) ||
+      (path != nullptr) != (len != nullptr) || wo < cap || (w_in && wi < cap) || (w_in == w_out && wi != wo) ||
       (int64_t)B * n * H > INT32_MAX || cache_rows > INT32_MAX)
     return KD_EINVAL;
-  int st = device_sms(nullptr);
+  int sms = 0, st = device_sms(&sms);
   if (st) return st;
-  aw::Params p{qa, qr, c, r, sc, sr, map, lens, path, len, vis, lse, w_in, w_out, wi, wo, dev_error, B, n, H, (n + 31) / 32, scale};
-  int64_t blocks = (map.cap + 7) / 8;
-  if (blocks > 4096) blocks = 4096;
-  aw::weights_kernel<<<dim3((unsigned)blocks, B), 256, 0, stream>>>(p);
-  return launch_status("weights_kernel");
+  int dev = 0;
+  if ((st = cuda_status(cudaGetDevice(&dev), "cudaGetDevice"))) return st;
+  static std::once_flag once[64];
+  static std::atomic<int> attr[64];
+  std::call_once(once[dev], [&] {
+    attr[dev].store(cuda_status(cudaFuncSetAttribute(aw::weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     aw::SMEM),
+                                "cudaFuncSetAttribute(weights_kernel)"));
+  });
+  if ((st = attr[dev].load())) return st;
+
+  aw::Params p;
+  p.lens = lens;
+  p.path = path;
+  p.len = len;
+  p.pt = pt;
+  p.vis = vis;
+  p.lse = lse;
+  p.w_in = w_in;
+  p.w_out = w_out;
+  p.err = dev_error;
+  p.cap = cap;
+  p.wi = wi;
+  p.wo = wo;
+  p.pages = pages;
+  p.B = B;
+  p.n = n;
+  p.H = H;
+  p.W = (n + 31) / 32;
+  p.P = pt ? page : 0;
+  p.M = (int)M;
+  p.Hp = (H + 15) / 16 * 16;
+  p.per_tile = aw::BN / p.Hp;
+  const int64_t rows = (int64_t)B * n * H;
+  const int tile_rows = (p.per_tile < n ? p.per_tile : n) * H;
+  p.linear = !path && H % 16 == 0 ? tile_rows : 0;
+  p.kbox = pt && page < aw::BK ? page : aw::BK;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const uint32_t qbox = (uint32_t)(p.linear ? p.linear : H);
+  CUtensorMap tqa, tqr, tc, tr;
+  if ((st = make_tmap3(&tqa, qa, KD_D_C, (uint64_t)rows, 1, KD_D_C, 0, qbox, 1))) return st;
+  if ((st = make_tmap3(&tqr, qr, KD_D_R, (uint64_t)rows, 1, KD_D_R, 0, qbox, 1))) return st;
+  if ((st = make_tmap3(&tc, c, KD_D_C, (uint64_t)cache_rows, 1, sc, 0, (uint32_t)p.kbox, 1))) return st;
+  if ((st = make_tmap3(&tr, r, KD_D_R, (uint64_t)cache_rows, 1, sr, 0, (uint32_t)p.kbox, 1))) return st;
+
+  // Cluster size: the one with the shortest longest run of query tiles, were every request
+  // of length cap.  A path is short as a rule (acceptance ends within a few nodes), so it
+  // counts as at most four nodes.
+  const int64_t units = B * ((cap + aw::BK - 1) / aw::BK);
+  const int nodes = path && n > 4 ? 4 : n;
+  const int64_t qt = (nodes + p.per_tile - 1) / p.per_tile;
+  int best = 1, fit = 0;
+  double cost = 1e300;
+  for (int cs = 1; cs <= aw::MAXC; cs *= 2) {
+    if (cs > 1 && cs > qt) break;
+    const int nc = active_clusters(cs, sms);
+    const double t = (double)((units + nc - 1) / nc) * ((double)((qt + cs - 1) / cs) + 0.3);
+    if (t < 0.95 * cost) cost = t, best = cs, fit = nc;
+  }
+  if (units > INT32_MAX) return KD_EINVAL;
+  const int64_t clusters = units < fit ? units : fit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * best));
+  cfg.blockDim = dim3(aw::THREADS);
+  cfg.dynamicSmemBytes = aw::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)best;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, aw::weights_kernel, tqa, tqr, tc, tr, p, best), "weights_kernel");
 }
 
 extern "C" int kd_kv_attn_weights(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* q_rope, const kd_bf16_t* c_kv,
@@ -101,9 +599,9 @@ extern "C" int kd_kv_attn_weights(const kd_bf16_t* q_nope_absorbed, const kd_bf1
                                   const int32_t* path, const int32_t* len, int B, int n, int H, float scale,
                                   const float* weights_in, int64_t w_in_stride, float* weights_out,
                                   int64_t w_out_stride, int32_t* dev_error, cudaStream_t stream) {
-  return weights_impl(q_nope_absorbed, q_rope, c_kv, k_rope, sc, sr, SlotMap{nullptr, cap, 0, 1, 0}, B * cap,
-                      cache_lens, vis, lse, path, len, B, n, H, scale, weights_in, w_in_stride, weights_out,
-                      w_out_stride, dev_error, stream);
+  return weights_impl(q_nope_absorbed, q_rope, c_kv, k_rope, sc, sr, cap, B * cap, nullptr, 0, 0, 0, cache_lens, vis,
+                      lse, path, len, B, n, H, scale, weights_in, w_in_stride, weights_out, w_out_stride, dev_error,
+                      stream);
 }
 
 extern "C" int kd_kv_attn_weights_paged(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* q_rope,
@@ -116,8 +614,7 @@ extern "C" int kd_kv_attn_weights_paged(const kd_bf16_t* q_nope_absorbed, const 
   if (!paged_ok(page_table, page_size, pages_per_req, num_pages) ||
       (page_size != 64 && page_size != 128 && page_size != 256))
     return KD_EINVAL;
-  return weights_impl(q_nope_absorbed, q_rope, c_pages, r_pages, sc, sr,
-                      SlotMap{page_table, pages_per_req * page_size, num_pages, page_size, (int)pages_per_req},
-                      num_pages * page_size, cache_lens, vis, lse, path, len, B, n, H, scale, weights_in, w_in_stride,
-                      weights_out, w_out_stride, dev_error, stream);
+  return weights_impl(q_nope_absorbed, q_rope, c_pages, r_pages, sc, sr, pages_per_req * page_size,
+                      num_pages * page_size, page_table, page_size, pages_per_req, num_pages, cache_lens, vis, lse,
+                      path, len, B, n, H, scale, weights_in, w_in_stride, weights_out, w_out_stride, dev_error, stream);
 }
