@@ -465,8 +465,9 @@ int kd_kv_norm_rope_write_paged(kd_bf16_t* c_pages, kd_bf16_t* r_pages, int64_t 
  *   out [T][H][128] bf16, lse [T][H] fp32, contiguous, not overlapping an input.
  * The keys and values of other sequences never enter a row, NaN or infinite ones
  * included, nor do the keys of later positions.  (A NaN or infinite v of a later position
- * of the row's own sequence can: it meets the weight 0 in the product.)  A sequence whose cumulative lengths are bad sets KD_DEV_BAD_SEQLENS and
- * its rows are left as they are.
+ * of the row's own sequence can: it meets the weight 0 in the product.)  Cumulative
+ * lengths that do not start at 0, decrease or pass T or Tk anywhere set
+ * KD_DEV_BAD_SEQLENS, and nothing is written.
  * Limits: T, Tk >= 0 (T = 0 enqueues nothing), T H and Tk Hk <= 2^31 - 1,
  * 1 <= B <= 65535, 1 <= H <= 128, Hk divides H, scale > 0; pointers 16-byte aligned,
  * strides multiples of 8.

@@ -174,23 +174,23 @@ def test_masked_keys_never_enter_inside_a_sequence(kd):
 
 
 @pytest.mark.gpu
-def test_bad_sequences_are_skipped(kd):
+def test_bad_cumulative_lengths_write_nothing(kd):
     q, k, v, _, _ = inputs([64], [64], 2, 1, False, seed=3)
     out = torch.full((64, 2, 128), 3.0, dtype=torch.bfloat16, device="cuda")
     lse, err = torch.full((64, 2), 4.0, device="cuda"), kd.new_error_word()
-    for cu, good in (([0, 20, 65], [(0, 20)]), ([0, 40, 30, 64], [(0, 40), (30, 34)]), ([-5, 10, 64], [(10, 54)]),
-                     ([0, 2 ** 31 - 1], [])):
-        out.fill_(3.0)
-        lse.fill_(4.0)
-        kd.kd_prompt_attn(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), out=out, lse=lse, dev_error=err)
+    good = [0, 20, 30, 64]
+    for cu, ck in (([0, 20, 30, 65], None), ([0, 40, 30, 64], None), ([-5, 10, 30, 64], None), ([1, 20, 30, 64], None),
+                   ([0, 2, 3, 2 ** 31 - 1], None), (good, [0, 10, 20, 65]), (good, [0, 20, 10, 64]), (good, [3, 10, 20, 64])):
+        kd.kd_prompt_attn(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), out=out, lse=lse, dev_error=err,
+                          cu_seqlens_k=None if ck is None else torch.tensor(ck, dtype=torch.int32, device="cuda"))
         assert kd.decode_device_error(kd.kd_read_device_error(err)) == ["BAD_SEQLENS"], cu
-        touched = torch.zeros(64, dtype=torch.bool, device="cuda")
-        for t, n in good:
-            touched[t:t + n] = True
-        assert bool((out[~touched] == 3.0).all()) and bool((lse[~touched] == 4.0).all())
-        if good and len(good) == 1:
-            t, n = good[0]
-            check(out[t:t + n], lse[t:t + n], q[t:t + n], k[t:t + n], v[t:t + n], [n], [n], 1.0 / math.sqrt(128.0))
+        assert bool((out == 3.0).all()) and bool((lse == 4.0).all())
+    kd.kd_prompt_attn(q, k[:50], v[:50], torch.tensor([0, 64], dtype=torch.int32, device="cuda"), out=out, lse=lse,
+                      dev_error=err)                    # fewer keys than the queries' lengths say
+    assert kd.decode_device_error(kd.kd_read_device_error(err)) == ["BAD_SEQLENS"]
+    kd.kd_prompt_attn(q, k, v, cu_of([64]), out=out, lse=lse, dev_error=err)
+    assert kd.kd_read_device_error(err) == 0
+    check(out, lse, q, k, v, [64], [64], 1.0 / math.sqrt(128.0))
 
 
 @pytest.mark.gpu

@@ -1,61 +1,493 @@
-// Causal attention of packed prompts with grouped heads, one warp per query row and
-// head: the keys one at a time under an online softmax.
+// Causal attention of packed prompts with grouped heads (tcgen05 + TMEM + TMA).
+//
+//   s_ij = scale (q_i . k_j), j <= i + nk - nq;  out_i = softmax(s_i) . v;  lse_i = ln sum exp s_ij
+//
+// A unit is (sequence, 256 query rows, head): two 128-row tiles that share every key and
+// value tile of 128 keys.  Each tile has its own score tile S (128 TMEM columns) and output
+// O (128 columns): 512 columns in all.  Each tile also has its own MMA warp and its own four
+// softmax warps (a thread per row), so that one tile's products run while the other's
+// exponentials do; two issuing warps also reach the tensor pipe's full rate at N = 128,
+// which one does not (72 cycles an MMA instead of 64).
+//
+// Per key tile the softmax warps copy S into registers, take the row maximum, and write
+// P = exp2(s - m) in bf16 over S's own columns, where it is the second product's A operand
+// from TMEM; the first half of the keys is handed over while the second is still being
+// computed.  The running maximum m only moves when it would rise by more than 8 (log2): P
+// stays below 2^8 and O is rescaled rarely, by the softmax warps themselves, between two
+// products (the commit that announced S also covers every earlier product into O).  The sum
+// is kept in fp32 from the unrounded exponentials; the rounding of P to bf16 is the type of
+// the MMA's operand.
+//
+// Shared memory: Q (two tiles of 128 rows), then a ring of 16 KB chunks through which keys
+// (128 keys x 64 columns) and values (64 keys x 128 columns) stream in the order they are
+// used.  Chunks are freed by both MMA warps.  Values past a sequence's last key are cleared
+// before they meet P = 0: what lies there belongs to another sequence.
+//
+// The grid has a block per possible unit, longest first inside a sequence; a block that is
+// done takes over the next one that has not started (cluster launch control), so that the
+// next unit's queries load and its scores begin while the last one's output is written.
+//
+// Every wait is bounded (kd_pipe.cuh).  No TMA multicast.
+
 #include <math.h>
 
-#include "kd_common.cuh"
-#include "kd_ptx.cuh"
+#include <atomic>
+
+#include "kd_pipe.cuh"
+#include "kd_tmap.cuh"
 
 namespace kd {
 namespace pr {
 
+using namespace ptx;
+
+constexpr int THREADS = 384;        // warps 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA, 9/10 MMA, 11 units
+constexpr int BM = 128, BN = 128;
+constexpr int CHUNK = 16384;
+constexpr int NS = 2;               // unit slots
+constexpr int MAXR = 10;            // ring chunks (8 with a rope part)
+
+enum Bar {
+  FULL = 0,                         // chunk landed (TMA)
+  FREE = FULL + MAXR,               // chunk used by both tiles (2 arrivals)
+  Q_FULL = FREE + MAXR,             // [2]
+  Q_FREE = Q_FULL + 2,              // [2] the unit's last QK MMA of the tile is done
+  S_FULL = Q_FREE + 2,              // [2]
+  P_FULL = S_FULL + 2,              // [2][2] half of P written (128 arrivals)
+  O_DONE = P_FULL + 4,              // [2] the unit's last PV MMA of the tile is done
+  U_FULL = O_DONE + 2,              // [NS] unit published
+  U_FREE = U_FULL + NS,             // [NS] unit read (11 arrivals: a lane of each other warp)
+  CLC = U_FREE + NS,                // the next block's answer arrived
+  DRAIN = CLC + 1,                  // [2]
+  NBAR = DRAIN + 2
+};
+constexpr int OFF_ABORT = 512, OFF_TMEM = 516, OFF_CLC = 528, OFF_UNIT = 544;
+constexpr int CTRL = 1024;
+constexpr int SMEM = CTRL + 1024 + 14 * CHUNK;      // Q and ring: 6 + 8 or 4 + 10 chunks
+static_assert(NBAR * 8 <= OFF_ABORT && OFF_UNIT + NS * 32 <= CTRL && SMEM <= 232448, "shared memory");
+
 struct Params {
-  const uint16_t *qn, *qr, *kn, *kr, *v;
-  int64_t qnt, qnh, qrt, qrh, knt, knh, krt, krh, vt, vh;
   const int32_t *cu_q, *cu_k;
   uint16_t* out;
   float* lse;
   int32_t* err;
-  int B, T, Tk, H, group;
-  float scale;
+  int B, T, Tk, H, group, slots;
+  int k_heads, r_heads, v_heads;      // 0: one head for all (head coordinate 0)
+  float scale, scale_log2;
 };
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+// What a unit is; n[i]: key tiles of query tile i.
+struct Unit {
+  int q0, nq, k0, nk, row, head;      // row: first query row of the unit inside its sequence
+  int n0, n1;
+  __device__ __forceinline__ int tiles(int i) const { return i ? n1 : n0; }
+};
 
-// blockIdx.y: sequence; warps over (row, head)
-__global__ void __launch_bounds__(256) prompt_kernel(const Params p) {
-  const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const int64_t q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-  const int64_t k0 = p.cu_k ? p.cu_k[b] : q0, k1 = p.cu_k ? p.cu_k[b + 1] : q1;
-  if (q0 < 0 || q1 < q0 || q1 > p.T || k0 < 0 || k1 < k0 || k1 > p.Tk) {
+// Key tiles that the 128 rows from `row` on see.
+__device__ __forceinline__ int tiles_of(int nq, int nk, int row) {
+  if (row >= nq) return 0;
+  const int last = min(row + BM, nq) - 1;
+  const int keys = min((int64_t)nk, (int64_t)last + nk - nq + 1);
+  return keys > 0 ? (keys + BN - 1) / BN : 0;
+}
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t a) { return smem_desc_sw128(a, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_v(uint32_t a) { return smem_desc_sw128(a, 8192, 1024); }
+
+__device__ __forceinline__ Unit read_unit(const uint8_t* gbase, int k) {
+  const int4* s = reinterpret_cast<const int4*>(gbase + OFF_UNIT + (k % NS) * 32);
+  const int4 a = s[0], b = s[1];
+  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+// Asks the hardware for a block that has not started; the answer lands at `dst` and completes 16 bytes on `bar`.
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+               "r"(bar)
+               : "memory");
+}
+// Block index in the answer, -1 when none was left.
+__device__ __forceinline__ int cancelled_block(uint32_t src) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.b32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(src)
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
+template <bool ROPE>
+__global__ void __launch_bounds__(THREADS, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
+              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+              const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  constexpr int KC = ROPE ? 3 : 2;            // 64-column chunks of a key
+  constexpr int RING = ROPE ? 8 : 10;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* gbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+  const uint32_t base = smem_u32(gbase);
+  const uint32_t q_smem = base + CTRL, ring = q_smem + 2 * KC * CHUNK;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
+  const Pipe pipe{base, abort_flag, p.err};
+
+  // cumulative lengths: all of them, by every block; a bad one ends the call
+  bool bad = false;
+  for (int b = threadIdx.x; b < p.B; b += THREADS) {
+    const int a = p.cu_q[b], z = p.cu_q[b + 1];
+    bad |= (b == 0 && a != 0) || a < 0 || z < a || z > p.T;
+    if (p.cu_k) {
+      const int ka = p.cu_k[b], kz = p.cu_k[b + 1];
+      bad |= (b == 0 && ka != 0) || ka < 0 || kz < ka || kz > p.Tk;
+    } else {
+      bad |= z > p.Tk;
+    }
+  }
+  if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0 && blockIdx.x == 0) raise_dev_error(p.err, KD_DEV_BAD_SEQLENS);
     return;
   }
-  const int64_t nq = q1 - q0, nk = k1 - k0;
-  for (int64_t w = blockIdx.x * 8 + (threadIdx.x >> 5); w < nq * p.H; w += (int64_t)gridDim.x * 8) {
-    const int64_t i = w / p.H;
-    const int h = (int)(w % p.H), g = h / p.group;
-    float q[4], r[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int e = 0; e < 4; ++e) q[e] = bf(p.qn[(q0 + i) * p.qnt + h * p.qnh + e * 32 + lane]);
-    if (p.qr)
-      for (int e = 0; e < 2; ++e) r[e] = bf(p.qr[(q0 + i) * p.qrt + h * p.qrh + e * 32 + lane]);
-    float m = -INFINITY, l = 0.f;
-    const int64_t end = min(nk, i + nk - nq + 1);
-    for (int64_t j = 0; j < end; ++j) {
-      float s = 0.f;
-      for (int e = 0; e < 4; ++e) s += q[e] * bf(p.kn[(k0 + j) * p.knt + g * p.knh + e * 32 + lane]);
-      if (p.qr)
-        for (int e = 0; e < 2; ++e) s += r[e] * bf(p.kr[(k0 + j) * p.krt + g * p.krh + e * 32 + lane]);
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= p.scale;
-      const float mn = fmaxf(m, s), c = m == mn ? 1.f : expf(m - mn), x = expf(s - mn);
-      l = l * c + x;
-      m = mn;
-      for (int e = 0; e < 4; ++e) o[e] = o[e] * c + x * bf(p.v[(k0 + j) * p.vt + g * p.vh + e * 32 + lane]);
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    for (int i = 0; i < NBAR; ++i) {
+      const int n = i >= FREE && i < FREE + MAXR ? 2 : i >= P_FULL && i < P_FULL + 4 ? 128
+                    : i >= U_FREE && i < U_FREE + NS ? 11 : 1;
+      mbar_init(base + 8 * i, n);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int e = 0; e < 4; ++e)
-      p.out[((q0 + i) * p.H + h) * 128 + e * 32 + lane] = (uint16_t)ptx::pack_bf16x2(o[e] * inv, 0.f);
-    if (lane == 0) p.lse[(q0 + i) * p.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    fence_mbar_init();
+  }
+  if (warp == 11) {
+    tmem_alloc(base + OFF_TMEM, 512);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    if (ROPE) {
+      tma_prefetch_desc(&tm_qr);
+      tma_prefetch_desc(&tm_kr);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM);
+  const uint32_t t_s = tmem, t_o = tmem + 2 * BN;
+
+  if (warp == 11) {
+    // ------------------------------------------------------------ units
+    int u = (int)blockIdx.x, k = 0, asks = 0;
+    bool ok = true;
+    while (true) {
+      if (lane == 0) {                                  // the next one, while this one is worked out
+        mbar_arrive_expect_tx(pipe.bar(CLC), 16);
+        try_cancel(base + OFF_CLC, pipe.bar(CLC));
+      }
+      // unit u: slot (256 rows) and head; sequence b has the slots from cu[b] / 256 + b on
+      const int slot = p.slots - 1 - u / p.H, head = u % p.H;
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.cu_q[mid] / (2 * BM) + mid <= slot) lo = mid;
+        else hi = mid - 1;
+      }
+      Unit w;
+      w.q0 = p.cu_q[lo];
+      w.nq = p.cu_q[lo + 1] - w.q0;
+      w.k0 = p.cu_k ? p.cu_k[lo] : w.q0;
+      w.nk = p.cu_k ? p.cu_k[lo + 1] - w.k0 : w.nq;
+      const int64_t row = (int64_t)(slot - w.q0 / (2 * BM) - lo) * (2 * BM);
+      if (row >= 0 && row < w.nq) {
+        w.row = (int)row;
+        if (!(ok = pipe.wait_warp(U_FREE + k % NS, ((k / NS) & 1) ^ 1))) break;
+        if (lane == 0) {
+          int4* s = reinterpret_cast<int4*>(gbase + OFF_UNIT + (k % NS) * 32);
+          s[0] = make_int4(w.q0, w.nq, w.k0, w.nk);
+          s[1] = make_int4(w.row, head, tiles_of(w.nq, w.nk, w.row), tiles_of(w.nq, w.nk, w.row + BM));
+          mbar_arrive(pipe.bar(U_FULL + k % NS));
+        }
+        __syncwarp();
+        ++k;
+      }
+      if (!(ok = pipe.wait_warp(CLC, asks & 1))) break;
+      ++asks;
+      u = cancelled_block(base + OFF_CLC);
+      fence_proxy_async_cta();                          // read before the next answer is written
+      __syncwarp();
+      if (u < 0) break;
+    }
+    if (!ok) {
+      pipe.drain(CLC, asks & 1);
+    } else if (pipe.wait_warp(U_FREE + k % NS, ((k / NS) & 1) ^ 1)) {
+      if (lane == 0) {
+        reinterpret_cast<int4*>(gbase + OFF_UNIT + (k % NS) * 32)[0] = make_int4(-1, 0, 0, 0);
+        mbar_arrive(pipe.bar(U_FULL + k % NS));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    uint32_t it = 0, nq[2] = {0, 0};
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
+      const Unit u = read_unit(gbase, k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
+      if (u.q0 < 0) break;
+      const int g = u.head / p.group, n = max(u.n0, u.n1);
+      auto load_q = [&](int i) -> bool {
+        if (u.tiles(i) == 0) return true;
+        if (!pipe.wait_warp(Q_FREE + i, (nq[i] & 1u) ^ 1u)) return false;
+        if (lane == 0) {
+          const uint32_t bar = pipe.bar(Q_FULL + i), dst = q_smem + i * KC * CHUNK;
+          const int row = u.q0 + u.row + i * BM;
+          mbar_arrive_expect_tx(bar, KC * CHUNK);
+          tma_load_3d(dst, &tm_q, 0, u.head, row, bar);
+          tma_load_3d(dst + CHUNK, &tm_q, 64, u.head, row, bar);
+          if (ROPE) tma_load_3d(dst + 2 * CHUNK, &tm_qr, 0, u.head, row, bar);
+        }
+        __syncwarp();
+        ++nq[i];
+        return true;
+      };
+      for (int j = 0; j < n && ok; ++j) {
+        const int key = u.k0 + j * BN;
+        if (j == 0 && !(ok = load_q(0))) break;
+        for (int c = 0; c < KC && ok; ++c, ++it) {
+          const uint32_t st = it % RING;
+          if (!(ok = pipe.wait_warp(FREE + st, ((it / RING) & 1u) ^ 1u))) break;
+          if (lane == 0) {
+            const uint32_t bar = pipe.bar(FULL + st), dst = ring + st * CHUNK;
+            mbar_arrive_expect_tx(bar, CHUNK);
+            if (c < 2) tma_load_3d(dst, &tm_k, c * 64, p.k_heads ? g : 0, key, bar);
+            else tma_load_3d(dst, &tm_kr, 0, p.r_heads ? g : 0, key, bar);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (j == 0 && !(ok = load_q(1))) break;
+        for (int h = 0; h < 2 && ok; ++h, ++it) {
+          const uint32_t st = it % RING;
+          if (!(ok = pipe.wait_warp(FREE + st, ((it / RING) & 1u) ^ 1u))) break;
+          if (lane == 0) {
+            const uint32_t bar = pipe.bar(FULL + st), dst = ring + st * CHUNK;
+            mbar_arrive_expect_tx(bar, CHUNK);
+            tma_load_3d(dst, &tm_v, 0, p.v_heads ? g : 0, key + h * 64, bar);
+            tma_load_3d(dst + CHUNK / 2, &tm_v, 64, p.v_heads ? g : 0, key + h * 64, bar);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    // every copy asked for lands before the block may leave
+    for (uint32_t j = it > RING ? it - RING : 0; j < it; ++j) pipe.drain(FULL + j % RING, (j / RING) & 1u);
+    for (int i = 0; i < 2; ++i)
+      if (nq[i]) pipe.drain(Q_FULL + i, (nq[i] - 1) & 1u);
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------ MMA of one tile
+    const int i = warp - 9;
+    const uint32_t d_s = t_s + i * BN, d_o = t_o + i * BN, q_at = q_smem + i * KC * CHUNK;
+    constexpr uint32_t IDESC_QK = idesc_bf16(BM, BN, 0, 0), IDESC_PV = idesc_bf16(BM, 128, 0, 1);
+    uint32_t it = 0, nu = 0, np = 0;            // ring position, units with work, key tiles
+    bool ok = true;
+    // S = Q K^T of key tile j; the K chunks follow each other in the ring
+    auto qk = [&](bool mine, bool last) -> bool {
+      for (int c = 0; c < KC; ++c, ++it) {
+        const uint32_t st = it % RING;
+        if (!pipe.wait_warp(FULL + st, (it / RING) & 1u)) return false;
+        if (lane == 0) {
+          if (mine) {
+            tc_fence_after();
+            const uint64_t a = desc_k(q_at + c * CHUNK), b = desc_k(ring + st * CHUNK);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) mma_bf16_ss(d_s, a + 2 * s, b + 2 * s, IDESC_QK, c + s > 0);
+            tc_commit(pipe.bar(FREE + st));
+          } else {
+            mbar_arrive(pipe.bar(FREE + st));
+          }
+        }
+        __syncwarp();
+      }
+      if (mine && lane == 0) {
+        tc_commit(pipe.bar(S_FULL + i));
+        if (last) tc_commit(pipe.bar(Q_FREE + i));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
+      const Unit u = read_unit(gbase, k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
+      if (u.q0 < 0) break;
+      const int n = u.tiles(i), all = max(u.n0, u.n1);
+      if (n > 0 && !(ok = pipe.wait_warp(Q_FULL + i, nu & 1u))) break;
+      if (all > 0 && !(ok = qk(n > 0, n == 1))) break;
+      for (int j = 0; j < all && ok; ++j) {
+        for (int h = 0; h < 2 && ok; ++h, ++it) {
+          const uint32_t st = it % RING;
+          const int keys = u.nk - j * BN - h * 64;      // keys of the sequence from this half on
+          if (j < n && !(ok = pipe.wait_warp(P_FULL + 2 * i + h, np & 1u))) break;
+          if (!(ok = pipe.wait_warp(FULL + st, (it / RING) & 1u))) break;
+          if (j < n && keys > 0 && keys < 64) {
+            // rows past the sequence's last key: cleared (a row is 128 bytes of each box;
+            // the swizzle stays inside it)
+            uint4* v = reinterpret_cast<uint4*>(gbase + (ring - base) + st * CHUNK);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              for (int e = keys * 8 + lane; e < 512; e += 32) v[q * 512 + e] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_cta();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            if (j < n && keys > 0) {
+              tc_fence_after();
+              const uint64_t b = desc_v(ring + st * CHUNK);
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma_bf16_ts(d_o, d_s + h * 32 + s * 8, b + s * 128, IDESC_PV, j + h + s > 0);
+              tc_commit(pipe.bar(FREE + st));
+            } else {
+              mbar_arrive(pipe.bar(FREE + st));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (j < n) ++np;
+        if (j + 1 < all) ok = qk(j + 1 < n, j + 2 == n);
+        else if (lane == 0 && n > 0) tc_commit(pipe.bar(O_DONE + i));
+        __syncwarp();
+      }
+      if (n > 0) ++nu;
+    }
+    if (lane == 0) tc_commit(pipe.bar(DRAIN + i));
+    __syncwarp();
+    pipe.drain(DRAIN + i, 0);                           // nothing in flight when TMEM is released
+  } else {
+    // ------------------------------------------------------------ softmax and output of one tile
+    const int i = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = t_s + i * BN + lanes, o_at = t_o + i * BN + lanes;
+    uint32_t ns = 0, nu = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
+      const Unit u = read_unit(gbase, k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
+      if (u.q0 < 0) break;
+      const int n = u.tiles(i), row = u.row + i * BM + r;
+      // keys this row sees, and those the tile's first row does
+      const int64_t off = (int64_t)u.nk - u.nq + 1;
+      const int lim = (int)max((int64_t)0, min((int64_t)u.nk, row + off));
+      const int lim0 = (int)max((int64_t)0, min((int64_t)u.nk, u.row + i * BM + off));
+      float m = -INFINITY, l = 0.f;                     // raw scores
+      for (int j = 0; j < n; ++j, ++ns) {
+        if (!(ok = pipe.wait_warp(S_FULL + i, ns & 1u))) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, *reinterpret_cast<uint32_t(*)[32]>(s + q * 32));
+        tmem_wait_ld();
+        if ((j + 1) * BN > lim0) {                      // some row of the tile does not see all of it
+          const int c0 = lim - j * BN;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] = c < c0 ? s[c] : 0xff800000u;
+        }
+        float mx = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+        float my = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
+#pragma unroll
+        for (int c = 4; c < 128; c += 4) {
+          mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          my = fmax3(my, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+        }
+        mx = fmaxf(mx, my);
+        // the maximum in use moves when P would pass 2^8
+        const bool rise = j == 0 || (mx - m) * p.scale_log2 > 8.f;
+        if (j > 0 && __any_sync(0xffffffffu, rise)) {
+          const float mn = rise ? mx : m;
+          const float f = rise ? ex2((m - mn) * p.scale_log2) : 1.f;       // m = -inf: 0
+          l *= f;
+          m = mn;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(o_at + q * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st32(o_at + q * 32, o);
+          }
+        } else if (j == 0) {
+          m = mx;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float a, b;
+            ffma2(a, b, __uint_as_float(s[h * 64 + 2 * c]), __uint_as_float(s[h * 64 + 2 * c + 1]), p.scale_log2, nm);
+            a = ex2(a);
+            b = ex2(b);
+            fadd2(l0, l1, a, b);
+            pk[c] = pack_bf16x2(a, b);
+          }
+          tmem_st32(s_at + h * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(pipe.bar(P_FULL + 2 * i + h));
+        }
+        l += l0 + l1;
+      }
+      if (!ok) break;
+      const bool mine = row < u.nq;
+      const int64_t at = ((int64_t)(u.q0 + row) * p.H + u.head);
+      if (n > 0) {
+        if (!(ok = pipe.wait_warp(O_DONE + i, nu & 1u))) break;
+        ++nu;
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);       // a NaN sum stays one
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[32];
+          tmem_ld32(o_at + q * 32, o);
+          tmem_wait_ld();
+          if (mine) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[c * 8 + 2 * e]) * inv,
+                                                   __uint_as_float(o[c * 8 + 2 * e + 1]) * inv);
+              st_global_v4(p.out + at * 128 + q * 32 + c * 8, v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+        tc_fence_before();
+      } else if (mine) {
+        for (int c = 0; c < 16; ++c) st_global_v4(p.out + at * 128 + c * 8, 0u, 0u, 0u, 0u);
+      }
+      if (mine) p.lse[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -64,8 +496,8 @@ __global__ void __launch_bounds__(256) prompt_kernel(const Params p) {
 
 using namespace kd;
 
-static bool view_ok(const void* p, int64_t tok, int64_t head) {
-  return p && aligned16(p) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0;
+static bool view_ok(const void* p, int64_t tok, int64_t head, int64_t rows) {
+  return p && aligned16(p) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0 && (tok > 0 || rows <= 1);
 }
 
 extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh, const kd_bf16_t* q_rope, int64_t qrt,
@@ -73,20 +505,55 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
                               int64_t krt, int64_t krh, const kd_bf16_t* v, int64_t vt, int64_t vh,
                               const int32_t* cu_q, const int32_t* cu_k, int B, int T, int Tk, int H, int Hk,
                               float scale, kd_bf16_t* out, float* lse, int32_t* dev_error, cudaStream_t stream) {
-  if (B < 1 || B > 65535 || T < 0 || Tk < 0 || H < 1 || H > KD_MAX_HEADS || Hk < 1 || H % Hk || !(scale > 0.f && isfinite(scale)) ||
-      (int64_t)T * H > INT32_MAX || (int64_t)Tk * Hk > INT32_MAX || (q_rope != nullptr) != (k_rope != nullptr))
+  if (B < 1 || B > 65535 || T < 0 || Tk < 0 || H < 1 || H > KD_MAX_HEADS || Hk < 1 || H % Hk ||
+      !(scale > 0.f && isfinite(scale)) || (int64_t)T * H > INT32_MAX || (int64_t)Tk * Hk > INT32_MAX ||
+      (q_rope != nullptr) != (k_rope != nullptr))
     return KD_EINVAL;
   if (T == 0) return KD_OK;
-  if (!view_ok(q_nope, qnt, qnh) || !out || !aligned16(out) || !lse || !cu_q ||
-      (Tk && (!view_ok(k_nope, knt, knh) || !view_ok(v, vt, vh))) ||
-      (q_rope && (!view_ok(q_rope, qrt, qrh) || (Tk && !view_ok(k_rope, krt, krh)))))
+  if (!view_ok(q_nope, qnt, qnh, T) || (H > 1 && qnh == 0) || !out || !aligned16(out) || !lse || !cu_q ||
+      (Tk && (!view_ok(k_nope, knt, knh, Tk) || !view_ok(v, vt, vh, Tk))) ||
+      (q_rope && (!view_ok(q_rope, qrt, qrh, T) || (H > 1 && qrh == 0) || (Tk && !view_ok(k_rope, krt, krh, Tk)))))
     return KD_EINVAL;
+  const int64_t slots = T / (2 * pr::BM) + (int64_t)B;
+  if (slots * H > INT32_MAX) return KD_EINVAL;
   int st = device_sms(nullptr);
   if (st) return st;
-  pr::Params p{q_nope, q_rope, k_nope, k_rope, v, qnt, qnh, qrt, qrh, knt, knh, krt, krh, vt, vh,
-               cu_q, cu_k, out, lse, dev_error, B, T, Tk, H, H / Hk, scale};
-  int64_t blocks = ((int64_t)T * H + 7) / 8;
-  if (blocks > 4096) blocks = 4096;
-  pr::prompt_kernel<<<dim3((unsigned)blocks, B), 256, 0, stream>>>(p);
+  int dev = 0;
+  if ((st = cuda_status(cudaGetDevice(&dev), "cudaGetDevice"))) return st;
+  static std::once_flag once[64];
+  static std::atomic<int> attr[64];
+  std::call_once(once[dev], [&] {
+    int s = cuda_status(cudaFuncSetAttribute(pr::prompt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             pr::SMEM),
+                        "cudaFuncSetAttribute(prompt_kernel)");
+    if (!s)
+      s = cuda_status(cudaFuncSetAttribute(pr::prompt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           pr::SMEM),
+                      "cudaFuncSetAttribute(prompt_kernel)");
+    attr[dev].store(s);
+  });
+  if ((st = attr[dev].load())) return st;
+
+  pr::Params p{cu_q, cu_k, out, lse, dev_error, B, T, Tk, H, H / Hk, (int)slots, knh > 0, krh > 0, vh > 0,
+               scale, scale * 1.4426950408889634f};
+  const bool rope = q_rope != nullptr;
+  CUtensorMap tq, tqr, tk, tkr, tv;
+  // without keys the key and value maps are never used: any memory will do
+  const kd_bf16_t *kp = Tk ? k_nope : q_nope, *vp = Tk ? v : q_nope, *rp = Tk ? k_rope : q_rope;
+  if ((st = make_tmap3(&tq, q_nope, 128, H, T, qnh, qnt, 1, pr::BM)) ||
+      (st = make_tmap3(&tk, kp, 128, knh ? Hk : 1, Tk, knh, knt, 1, pr::BN)) ||
+      (st = make_tmap3(&tv, vp, 128, vh ? Hk : 1, Tk, vh, vt, 1, 64)))
+    return st;
+  if (rope) {
+    if ((st = make_tmap3(&tqr, q_rope, 64, H, T, qrh, qrt, 1, pr::BM)) ||
+        (st = make_tmap3(&tkr, rp, 64, krh ? Hk : 1, Tk, krh, krt, 1, pr::BN)))
+      return st;
+  } else {
+    tqr = tq;
+    tkr = tk;
+  }
+  const unsigned grid = (unsigned)(slots * H);
+  if (rope) pr::prompt_kernel<true><<<grid, pr::THREADS, pr::SMEM, stream>>>(tq, tqr, tk, tkr, tv, p);
+  else pr::prompt_kernel<false><<<grid, pr::THREADS, pr::SMEM, stream>>>(tq, tqr, tk, tkr, tv, p);
   return launch_status("prompt_kernel");
 }
