@@ -20,7 +20,7 @@
 //
 // Shared memory: Q (two tiles of 128 rows), then a ring of 16 KB chunks through which keys
 // (128 keys x 64 columns) and values (64 keys x 128 columns) stream in the order they are
-// used.  Chunks are freed by both MMA warps.  Values past a sequence's last key are cleared
+// used.  Values past a sequence's last key are cleared
 // before they meet P = 0: what lies there belongs to another sequence.
 //
 // The grid has a block per possible unit, longest first inside a sequence; a block that is
@@ -41,25 +41,28 @@ namespace pr {
 
 using namespace ptx;
 
-constexpr int THREADS = 384;        // warps 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA, 9/10 MMA, 11 units
+constexpr int THREADS = 384;        // warps 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA, 9 MMA, 11 units
 constexpr int BM = 128, BN = 128;
 constexpr int CHUNK = 16384;
 constexpr int NS = 2;               // unit slots
-constexpr int MAXR = 10;            // ring chunks (8 with a rope part)
+constexpr int NO = 4;               // barriers of key (value) tiles in flight: a power of two, at least what the ring holds
 
 enum Bar {
-  FULL = 0,                         // chunk landed (TMA)
-  FREE = FULL + MAXR,               // chunk used by both tiles (2 arrivals)
-  Q_FULL = FREE + MAXR,             // [2]
+  K_FULL = 0,                       // [NO] a key tile's keys landed (TMA)
+  K_FREE = K_FULL + NO,             // [NO] both query tiles' scores are done
+  V_FULL = K_FREE + NO,             // [NO] its values
+  V_FREE = V_FULL + NO,             // [NO]
+  Q_FULL = V_FREE + NO,             // [2]
   Q_FREE = Q_FULL + 2,              // [2] the unit's last QK MMA of the tile is done
   S_FULL = Q_FREE + 2,              // [2]
   P_FULL = S_FULL + 2,              // [2][2] half of P written (128 arrivals)
   O_DONE = P_FULL + 4,              // [2] the unit's last PV MMA of the tile is done
   U_FULL = O_DONE + 2,              // [NS] unit published
-  U_FREE = U_FULL + NS,             // [NS] unit read (11 arrivals: a lane of each other warp)
-  CLC = U_FREE + NS,                // the next block's answer arrived
-  DRAIN = CLC + 1,                  // [2]
-  NBAR = DRAIN + 2
+  U_FREE = U_FULL + NS,             // [NS] unit read (10 arrivals: a lane of each reading warp)
+  TURN = U_FREE + NS,               // [2][4] a tile's warp has issued a key tile's exponentials
+  CLC = TURN + 8,                   // the next block's answer arrived
+  DRAIN = CLC + 1,
+  NBAR = DRAIN + 1
 };
 constexpr int OFF_ABORT = 512, OFF_TMEM = 516, OFF_CLC = 528, OFF_UNIT = 544;
 constexpr int CTRL = 1024;
@@ -83,6 +86,10 @@ struct Unit {
   __device__ __forceinline__ int tiles(int i) const { return i ? n1 : n0; }
 };
 
+// Chunk index inside a ring of N.
+template <int N>
+__device__ __forceinline__ uint32_t wrap(uint32_t x) { return x >= N ? x - N : x; }
+
 // Key tiles that the 128 rows from `row` on see.
 __device__ __forceinline__ int tiles_of(int nq, int nk, int row) {
   if (row >= nq) return 0;
@@ -94,10 +101,16 @@ __device__ __forceinline__ int tiles_of(int nq, int nk, int row) {
 __device__ __forceinline__ uint64_t desc_k(uint32_t a) { return smem_desc_sw128(a, 16, 1024); }
 __device__ __forceinline__ uint64_t desc_v(uint32_t a) { return smem_desc_sw128(a, 8192, 1024); }
 
+// A value all lanes hold, as one the compiler knows to be the same in all of them: what the
+// MMAs' operands and the loops around them are made of then stays in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ Unit read_unit(const uint8_t* gbase, int k) {
   const int4* s = reinterpret_cast<const int4*>(gbase + OFF_UNIT + (k % NS) * 32);
   const int4 a = s[0], b = s[1];
-  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return Unit{uniform(a.x), uniform(a.y), uniform(a.z), uniform(a.w),
+              uniform(b.x), uniform(b.y), uniform(b.z), uniform(b.w)};
 }
 
 // Asks the hardware for a block that has not started; the answer lands at `dst` and completes 16 bytes on `bar`.
@@ -132,7 +145,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   uint8_t* gbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
   const uint32_t base = smem_u32(gbase);
   const uint32_t q_smem = base + CTRL, ring = q_smem + 2 * KC * CHUNK;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
   const Pipe pipe{base, abort_flag, p.err};
 
@@ -155,8 +168,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     for (int i = 0; i < NBAR; ++i) {
-      const int n = i >= FREE && i < FREE + MAXR ? 2 : i >= P_FULL && i < P_FULL + 4 ? 128
-                    : i >= U_FREE && i < U_FREE + NS ? 11 : 1;
+      const int n = i >= P_FULL && i < P_FULL + 4 ? 128
+                    : i >= U_FREE && i < U_FREE + NS ? 10 : 1;
       mbar_init(base + 8 * i, n);
     }
     fence_mbar_init();
@@ -177,7 +190,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM);
+  const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM));
   const uint32_t t_s = tmem, t_o = tmem + 2 * BN;
 
   if (warp == 11) {
@@ -233,8 +246,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ loads
-    uint32_t it = 0, nq[2] = {0, 0};
+    uint32_t kt = 0, nk = 0, nv = 0, nq[2] = {0, 0};    // key tiles; keys, values and queries asked for
+    uint32_t pos = 0, used = 0, fk = 0, fv = 0;         // ring: next chunk, chunks held; keys and values freed
     bool ok = true;
+    // makes room for `chunks` more; what is freed is freed in the order it was loaded
+    auto room = [&](uint32_t chunks) -> bool {
+      while (used + chunks > RING) {
+        if (fk == fv) {
+          if (!pipe.wait_warp(K_FREE + fk % NO, (fk / NO) & 1u)) return false;
+          ++fk;
+          used -= KC;
+        } else {
+          if (!pipe.wait_warp(V_FREE + fv % NO, (fv / NO) & 1u)) return false;
+          ++fv;
+          used -= 2;
+        }
+      }
+      used += chunks;
+      return true;
+    };
     for (int k = 0; ok; ++k) {
       if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
       const Unit u = read_unit(gbase, k);
@@ -257,69 +287,92 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         ++nq[i];
         return true;
       };
-      for (int j = 0; j < n && ok; ++j) {
+      for (int j = 0; j < n; ++j, ++kt) {
         const int key = u.k0 + j * BN;
+        const uint32_t o = kt % NO;
         if (j == 0 && !(ok = load_q(0))) break;
-        for (int c = 0; c < KC && ok; ++c, ++it) {
-          const uint32_t st = it % RING;
-          if (!(ok = pipe.wait_warp(FREE + st, ((it / RING) & 1u) ^ 1u))) break;
-          if (lane == 0) {
-            const uint32_t bar = pipe.bar(FULL + st), dst = ring + st * CHUNK;
-            mbar_arrive_expect_tx(bar, CHUNK);
+        if (!(ok = room(KC))) break;
+        if (lane == 0) {
+          const uint32_t bar = pipe.bar(K_FULL + o);
+          mbar_arrive_expect_tx(bar, KC * CHUNK);
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const uint32_t dst = ring + wrap<RING>(pos + c) * CHUNK;
             if (c < 2) tma_load_3d(dst, &tm_k, c * 64, p.k_heads ? g : 0, key, bar);
             else tma_load_3d(dst, &tm_kr, 0, p.r_heads ? g : 0, key, bar);
           }
-          __syncwarp();
         }
-        if (!ok) break;
+        __syncwarp();
+        pos = wrap<RING>(pos + KC);
+        ++nk;
         if (j == 0 && !(ok = load_q(1))) break;
-        for (int h = 0; h < 2 && ok; ++h, ++it) {
-          const uint32_t st = it % RING;
-          if (!(ok = pipe.wait_warp(FREE + st, ((it / RING) & 1u) ^ 1u))) break;
-          if (lane == 0) {
-            const uint32_t bar = pipe.bar(FULL + st), dst = ring + st * CHUNK;
-            mbar_arrive_expect_tx(bar, CHUNK);
+        if (!(ok = room(2))) break;
+        if (lane == 0) {
+          const uint32_t bar = pipe.bar(V_FULL + o);
+          mbar_arrive_expect_tx(bar, 2 * CHUNK);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t dst = ring + wrap<RING>(pos + h) * CHUNK;
             tma_load_3d(dst, &tm_v, 0, p.v_heads ? g : 0, key + h * 64, bar);
             tma_load_3d(dst + CHUNK / 2, &tm_v, 64, p.v_heads ? g : 0, key + h * 64, bar);
           }
-          __syncwarp();
         }
+        __syncwarp();
+        pos = wrap<RING>(pos + 2);
+        ++nv;
       }
     }
     // every copy asked for lands before the block may leave
-    for (uint32_t j = it > RING ? it - RING : 0; j < it; ++j) pipe.drain(FULL + j % RING, (j / RING) & 1u);
+    for (uint32_t o = nk > NO ? nk - NO : 0; o < nk; ++o) pipe.drain(K_FULL + o % NO, (o / NO) & 1u);
+    for (uint32_t o = nv > NO ? nv - NO : 0; o < nv; ++o) pipe.drain(V_FULL + o % NO, (o / NO) & 1u);
     for (int i = 0; i < 2; ++i)
       if (nq[i]) pipe.drain(Q_FULL + i, (nq[i] - 1) & 1u);
-  } else if (warp == 9 || warp == 10) {
-    // ------------------------------------------------------------ MMA of one tile
-    const int i = warp - 9;
-    const uint32_t d_s = t_s + i * BN, d_o = t_o + i * BN, q_at = q_smem + i * KC * CHUNK;
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA
     constexpr uint32_t IDESC_QK = idesc_bf16(BM, BN, 0, 0), IDESC_PV = idesc_bf16(BM, 128, 0, 1);
-    uint32_t it = 0, nu = 0, np = 0;            // ring position, units with work, key tiles
+    uint32_t kt = 0, pos = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // key tiles, ring, units with work, P tiles
     bool ok = true;
-    // S = Q K^T of key tile j; the K chunks follow each other in the ring
-    auto qk = [&](bool mine, bool last) -> bool {
-      for (int c = 0; c < KC; ++c, ++it) {
-        const uint32_t st = it % RING;
-        if (!pipe.wait_warp(FULL + st, (it / RING) & 1u)) return false;
-        if (lane == 0) {
-          if (mine) {
-            tc_fence_after();
-            const uint64_t a = desc_k(q_at + c * CHUNK), b = desc_k(ring + st * CHUNK);
+    // S = Q K^T of one tile; `at`: chunk where the keys begin
+    auto qk = [&](int i, uint32_t at, bool last) {
+      if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) mma_bf16_ss(d_s, a + 2 * s, b + 2 * s, IDESC_QK, c + s > 0);
-            tc_commit(pipe.bar(FREE + st));
-          } else {
-            mbar_arrive(pipe.bar(FREE + st));
-          }
+        for (int c = 0; c < KC; ++c) {
+          const uint64_t a = desc_k(q_smem + (i * KC + c) * CHUNK), b = desc_k(ring + wrap<RING>(at + c) * CHUNK);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) mma_bf16_ss(t_s + i * BN, a + 2 * s, b + 2 * s, IDESC_QK, c + s > 0);
         }
-        __syncwarp();
-      }
-      if (mine && lane == 0) {
         tc_commit(pipe.bar(S_FULL + i));
         if (last) tc_commit(pipe.bar(Q_FREE + i));
       }
       __syncwarp();
+    };
+    // O += P V of one tile; keys: the sequence's keys from this key tile on
+    auto pv = [&](int i, uint32_t at, int j, int keys) -> bool {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v = ring + wrap<RING>(at + h) * CHUNK;
+        if (!pipe.wait_warp(P_FULL + 2 * i + h, np[i] & 1u)) return false;
+        if (keys - h * 64 <= 0) continue;
+        if (keys - h * 64 < 64) {
+          // rows past the sequence's last key: cleared (a row is 128 bytes of each box; the
+          // swizzle stays inside it)
+          uint4* z = reinterpret_cast<uint4*>(gbase + (v - base));
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            for (int e = (keys - h * 64) * 8 + lane; e < 512; e += 32) z[q * 512 + e] = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_cta();
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t b = desc_v(v);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma_bf16_ts(t_o + i * BN, t_s + i * BN + h * 32 + s * 8, b + s * 128, IDESC_PV, j + h + s > 0);
+        }
+        __syncwarp();
+      }
+      ++np[i];
       return true;
     };
     for (int k = 0; ok; ++k) {
@@ -328,56 +381,54 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
-      const int n = u.tiles(i), all = max(u.n0, u.n1);
-      if (n > 0 && !(ok = pipe.wait_warp(Q_FULL + i, nu & 1u))) break;
-      if (all > 0 && !(ok = qk(n > 0, n == 1))) break;
-      for (int j = 0; j < all && ok; ++j) {
-        for (int h = 0; h < 2 && ok; ++h, ++it) {
-          const uint32_t st = it % RING;
-          const int keys = u.nk - j * BN - h * 64;      // keys of the sequence from this half on
-          if (j < n && !(ok = pipe.wait_warp(P_FULL + 2 * i + h, np & 1u))) break;
-          if (!(ok = pipe.wait_warp(FULL + st, (it / RING) & 1u))) break;
-          if (j < n && keys > 0 && keys < 64) {
-            // rows past the sequence's last key: cleared (a row is 128 bytes of each box;
-            // the swizzle stays inside it)
-            uint4* v = reinterpret_cast<uint4*>(gbase + (ring - base) + st * CHUNK);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              for (int e = keys * 8 + lane; e < 512; e += 32) v[q * 512 + e] = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_cta();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            if (j < n && keys > 0) {
-              tc_fence_after();
-              const uint64_t b = desc_v(ring + st * CHUNK);
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                mma_bf16_ts(d_o, d_s + h * 32 + s * 8, b + s * 128, IDESC_PV, j + h + s > 0);
-              tc_commit(pipe.bar(FREE + st));
-            } else {
-              mbar_arrive(pipe.bar(FREE + st));
-            }
-          }
+      const int all = max(u.n0, u.n1);
+      if (all == 0) continue;
+      if (!(ok = pipe.wait_warp(K_FULL + kt % NO, (kt / NO) & 1u))) break;
+      for (int i = 0; i < 2 && ok; ++i)
+        if (u.tiles(i) > 0) {
+          if (!(ok = pipe.wait_warp(Q_FULL + i, nu[i] & 1u))) break;
+          tc_fence_after();
+          qk(i, pos, u.tiles(i) == 1);
+          ++nu[i];
+        }
+      if (!ok) break;
+      if (elect_one()) tc_commit(pipe.bar(K_FREE + kt % NO));
+      __syncwarp();
+      for (int j = 0; j < all; ++j, ++kt) {
+        const uint32_t v_at = wrap<RING>(pos + KC), next = wrap<RING>(v_at + 2), o = kt % NO, o1 = (kt + 1) % NO;
+        if (!(ok = pipe.wait_warp(V_FULL + o, (kt / NO) & 1u))) break;
+        if (j < u.n0) {
+          if (!(ok = pv(0, v_at, j, u.nk - j * BN))) break;
+          if (j + 1 < all && !(ok = pipe.wait_warp(K_FULL + o1, ((kt + 1) / NO) & 1u))) break;
+          if (j + 1 < u.n0) qk(0, next, j + 2 == u.n0);
+          else if (elect_one()) tc_commit(pipe.bar(O_DONE));
+          __syncwarp();
+        } else if (j + 1 < all && !(ok = pipe.wait_warp(K_FULL + o1, ((kt + 1) / NO) & 1u))) {
+          break;
+        }
+        if (j < u.n1 && !(ok = pv(1, v_at, j, u.nk - j * BN))) break;
+        if (elect_one()) tc_commit(pipe.bar(V_FREE + o));       // both tiles are past these values
+        __syncwarp();
+        if (j < u.n1) {
+          if (j + 1 < u.n1) qk(1, next, j + 2 == u.n1);
+          else if (elect_one()) tc_commit(pipe.bar(O_DONE + 1));
           __syncwarp();
         }
-        if (!ok) break;
-        if (j < n) ++np;
-        if (j + 1 < all) ok = qk(j + 1 < n, j + 2 == n);
-        else if (lane == 0 && n > 0) tc_commit(pipe.bar(O_DONE + i));
+        if (j + 1 < all && elect_one()) tc_commit(pipe.bar(K_FREE + o1));
         __syncwarp();
+        pos = next;
       }
-      if (n > 0) ++nu;
     }
-    if (lane == 0) tc_commit(pipe.bar(DRAIN + i));
+    if (elect_one()) tc_commit(pipe.bar(DRAIN));
     __syncwarp();
-    pipe.drain(DRAIN + i, 0);                           // nothing in flight when TMEM is released
-  } else {
+    pipe.drain(DRAIN, 0);                               // nothing in flight when TMEM is released
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax and output of one tile
     const int i = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = t_s + i * BN + lanes, o_at = t_o + i * BN + lanes;
-    uint32_t ns = 0, nu = 0;
+    const int my_turn = TURN + 4 * i + (warp & 3), other = TURN + 4 * (i ^ 1) + (warp & 3);
+    uint32_t ns = 0, nu = 0, nt = 0;                    // key tiles, units with work, turns waited for
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
@@ -385,7 +436,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
-      const int n = u.tiles(i), row = u.row + i * BM + r;
+      const int n = u.tiles(i), row = u.row + i * BM + r, both = min(u.n0, u.n1);
       // keys this row sees, and those the tile's first row does
       const int64_t off = (int64_t)u.nk - u.nq + 1;
       const int lim = (int)max((int64_t)0, min((int64_t)u.nk, row + off));
@@ -403,14 +454,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
           for (int c = 0; c < 128; ++c) s[c] = c < c0 ? s[c] : 0xff800000u;
         }
-        float mx = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
-        float my = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
+        float mv[4];                                    // four chains: the latency of one would show
 #pragma unroll
-        for (int c = 4; c < 128; c += 4) {
-          mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          my = fmax3(my, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        }
-        mx = fmaxf(mx, my);
+        for (int q = 0; q < 4; ++q) mv[q] = fmaxf(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1]));
+#pragma unroll
+        for (int c = 8; c < 128; c += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mv[q] = fmax3(mv[q], __uint_as_float(s[c + 2 * q]), __uint_as_float(s[c + 2 * q + 1]));
+        const float mx = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
         // the maximum in use moves when P would pass 2^8
         const bool rise = j == 0 || (mx - m) * p.scale_log2 > 8.f;
         if (j > 0 && __any_sync(0xffffffffu, rise)) {
@@ -432,6 +484,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
         float l0 = 0.f, l1 = 0.f;
+        // the two tiles' warps of one scheduler take turns at the exponentials: tile 1 after
+        // tile 0 of the same key tile, tile 0 after tile 1 of the one before
+        if (j < both && (i == 1 || j > 0)) {
+          if (!(ok = pipe.wait_warp(other, nt & 1u))) break;
+          ++nt;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
@@ -444,6 +502,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             fadd2(l0, l1, a, b);
             pk[c] = pack_bf16x2(a, b);
           }
+          if (h == 1 && lane == 0 && (i == 0 ? j < both : j + 1 < both)) mbar_arrive(pipe.bar(my_turn));
           tmem_st32(s_at + h * 32, pk);
           tmem_wait_st();
           tc_fence_before();
