@@ -469,8 +469,9 @@ int kd_kv_norm_rope_write_paged(kd_bf16_t* c_pages, kd_bf16_t* r_pages, int64_t 
  * lengths that do not start at 0, decrease or pass T or Tk anywhere set
  * KD_DEV_BAD_SEQLENS, and nothing is written.
  * Limits: T, Tk >= 0 (T = 0 enqueues nothing), T H and Tk Hk <= 2^31 - 1,
- * 1 <= B <= 65535, 1 <= H <= 128, Hk divides H, scale > 0; pointers 16-byte aligned,
- * strides multiples of 8.
+ * 1 <= B <= 65535, 1 <= H <= 128, Hk divides H, scale > 0 and finite; pointers 16-byte
+ * aligned (out: 32), strides multiples of 8, those of queries not 0; H (T / 256 + B)
+ * <= 2^31 - 1.
  */
 int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qn_tok_stride, int64_t qn_head_stride,
                    const kd_bf16_t* q_rope, int64_t qr_tok_stride, int64_t qr_head_stride,

@@ -81,10 +81,10 @@ def lib():
 def test_host_validation(lib):
     V = ctypes.c_void_p
     ok = [V(16), 512, 128, V(16), 256, 64, V(16), 512, 128, V(16), 64, 0, V(16), 512, 128, V(16), None, 2, 10, 10, 4, 2,
-          0.1, V(16), V(16), None, None]
+          0.1, V(32), V(16), None, None]
     for i, v in ((0, None), (0, V(8)), (1, 9), (2, -8), (3, None), (4, 4), (6, None), (9, None), (12, V(20)), (13, 1),
                  (15, None), (17, 0), (17, 65536), (18, -1), (19, -1), (20, 0), (20, 129), (20, 3), (21, 0), (21, 8),
-                 (22, 0.0), (22, float("nan")), (22, float("inf")), (23, None), (23, V(8)), (24, None)):
+                 (22, 0.0), (22, float("nan")), (22, float("inf")), (23, None), (23, V(48)), (24, None)):
         bad = list(ok)
         bad[i] = v
         assert lib.kd_prompt_attn(*bad) == -1, i

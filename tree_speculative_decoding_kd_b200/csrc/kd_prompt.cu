@@ -60,7 +60,8 @@ enum Bar {
   U_FULL = O_DONE + 2,              // [NS] unit published
   U_FREE = U_FULL + NS,             // [NS] unit read (10 arrivals: a lane of each reading warp)
   TURN = U_FREE + NS,               // [2][4] a tile's warp has issued a key tile's exponentials
-  CLC = TURN + 8,                   // the next block's answer arrived
+  GO = TURN + 8,                    // the unit's last loads are near: time to claim the next one
+  CLC = GO + 1,                     // the next block's answer arrived
   DRAIN = CLC + 1,
   NBAR = DRAIN + 1
 };
@@ -198,10 +199,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     int u = (int)blockIdx.x, k = 0, asks = 0;
     bool ok = true;
     while (true) {
-      if (lane == 0) {                                  // the next one, while this one is worked out
-        mbar_arrive_expect_tx(pipe.bar(CLC), 16);
-        try_cancel(base + OFF_CLC, pipe.bar(CLC));
-      }
       // unit u: slot (256 rows) and head; sequence b has the slots from cu[b] / 256 + b on
       const int slot = p.slots - 1 - u / p.H, head = u % p.H;
       int lo = 0, hi = p.B - 1;
@@ -226,18 +223,26 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           mbar_arrive(pipe.bar(U_FULL + k % NS));
         }
         __syncwarp();
+        // claimed late: a block that holds units it has not begun leaves the others idle at the end
+        if (!(ok = pipe.wait_warp(GO, k & 1))) break;
         ++k;
       }
-      if (!(ok = pipe.wait_warp(CLC, asks & 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(pipe.bar(CLC), 16);
+        try_cancel(base + OFF_CLC, pipe.bar(CLC));
+      }
+      __syncwarp();
+      if (!(ok = pipe.wait_warp(CLC, asks & 1))) {
+        pipe.drain(CLC, asks & 1);
+        break;
+      }
       ++asks;
       u = cancelled_block(base + OFF_CLC);
       fence_proxy_async_cta();                          // read before the next answer is written
       __syncwarp();
       if (u < 0) break;
     }
-    if (!ok) {
-      pipe.drain(CLC, asks & 1);
-    } else if (pipe.wait_warp(U_FREE + k % NS, ((k / NS) & 1) ^ 1)) {
+    if (ok && pipe.wait_warp(U_FREE + k % NS, ((k / NS) & 1) ^ 1)) {
       if (lane == 0) {
         reinterpret_cast<int4*>(gbase + OFF_UNIT + (k % NS) * 32)[0] = make_int4(-1, 0, 0, 0);
         mbar_arrive(pipe.bar(U_FULL + k % NS));
@@ -272,6 +277,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
       const int g = u.head / p.group, n = max(u.n0, u.n1);
+      if (n == 0 && lane == 0) mbar_arrive(pipe.bar(GO));
       auto load_q = [&](int i) -> bool {
         if (u.tiles(i) == 0) return true;
         if (!pipe.wait_warp(Q_FREE + i, (nq[i] & 1u) ^ 1u)) return false;
@@ -290,6 +296,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       for (int j = 0; j < n; ++j, ++kt) {
         const int key = u.k0 + j * BN;
         const uint32_t o = kt % NO;
+        if (j == max(n - 2, 0) && lane == 0) mbar_arrive(pipe.bar(GO));
         if (j == 0 && !(ok = load_q(0))) break;
         if (!(ok = room(KC))) break;
         if (lane == 0) {
@@ -525,13 +532,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           tmem_wait_ld();
           if (mine) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[4];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[c * 8 + 2 * e]) * inv,
-                                                   __uint_as_float(o[c * 8 + 2 * e + 1]) * inv);
-              st_global_v4(p.out + at * 128 + q * 32 + c * 8, v[0], v[1], v[2], v[3]);
+              for (int e = 0; e < 8; ++e)
+                v[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[c * 16 + 2 * e]) * inv,
+                                                   __uint_as_float(o[c * 16 + 2 * e + 1]) * inv);
+              st_global_v8(p.out + at * 128 + q * 32 + c * 16, v);
             }
           }
         }
@@ -569,7 +576,7 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
       (q_rope != nullptr) != (k_rope != nullptr))
     return KD_EINVAL;
   if (T == 0) return KD_OK;
-  if (!view_ok(q_nope, qnt, qnh, T) || (H > 1 && qnh == 0) || !out || !aligned16(out) || !lse || !cu_q ||
+  if (!view_ok(q_nope, qnt, qnh, T) || (H > 1 && qnh == 0) || !out || (reinterpret_cast<uintptr_t>(out) & 31u) || !lse || !cu_q ||
       (Tk && (!view_ok(k_nope, knt, knh, Tk) || !view_ok(v, vt, vh, Tk))) ||
       (q_rope && (!view_ok(q_rope, qrt, qrh, T) || (H > 1 && qrh == 0) || (Tk && !view_ok(k_rope, krt, krh, Tk)))))
     return KD_EINVAL;
