@@ -41,7 +41,7 @@ namespace pr {
 
 using namespace ptx;
 
-constexpr int THREADS = 384;        // warps 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA, 9 MMA, 11 units
+constexpr int THREADS = 384;        // warps 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA, 9 MMA, 10 clears, 11 units
 constexpr int BM = 128, BN = 128;
 constexpr int CHUNK = 16384;
 constexpr int NS = 2;               // unit slots
@@ -52,13 +52,15 @@ enum Bar {
   K_FREE = K_FULL + NO,             // [NO] both query tiles' scores are done
   V_FULL = K_FREE + NO,             // [NO] its values
   V_FREE = V_FULL + NO,             // [NO]
-  Q_FULL = V_FREE + NO,             // [2]
+  V_CLEAN = V_FREE + NO,            // the rows past a sequence's last key are cleared
+  V_GO = V_CLEAN + 1,               // the tile before it is in work
+  Q_FULL = V_GO + 1,                // [2]
   Q_FREE = Q_FULL + 2,              // [2] the unit's last QK MMA of the tile is done
   S_FULL = Q_FREE + 2,              // [2]
   P_FULL = S_FULL + 2,              // [2][2] half of P written (128 arrivals)
   O_DONE = P_FULL + 4,              // [2] the unit's last PV MMA of the tile is done
   U_FULL = O_DONE + 2,              // [NS] unit published
-  U_FREE = U_FULL + NS,             // [NS] unit read (10 arrivals: a lane of each reading warp)
+  U_FREE = U_FULL + NS,             // [NS] unit read (11 arrivals: a lane of each other warp)
   TURN = U_FREE + NS,               // [2][4] a tile's warp has issued a key tile's exponentials
   GO = TURN + 8,                    // the unit's last loads are near: time to claim the next one
   CLC = GO + 1,                     // the next block's answer arrived
@@ -170,7 +172,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     *abort_flag = 0u;
     for (int i = 0; i < NBAR; ++i) {
       const int n = i >= P_FULL && i < P_FULL + 4 ? 128
-                    : i >= U_FREE && i < U_FREE + NS ? 10 : 1;
+                    : i >= U_FREE && i < U_FREE + NS ? 11 : 1;
       mbar_init(base + 8 * i, n);
     }
     fence_mbar_init();
@@ -335,13 +337,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     for (int i = 0; i < 2; ++i)
       if (nq[i]) pipe.drain(Q_FULL + i, (nq[i] - 1) & 1u);
   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA
-    constexpr uint32_t IDESC_QK = idesc_bf16(BM, BN, 0, 0), IDESC_PV = idesc_bf16(BM, 128, 0, 1);
-    uint32_t kt = 0, pos = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // key tiles, ring, units with work, P tiles
-    bool ok = true;
-    // S = Q K^T of one tile; `at`: chunk where the keys begin
-    auto qk = [&](int i, uint32_t at, bool last) {
-      if (elect_one()) {
+    // ------------------------------------------------------------ MMA (one thread)
+    // Its scalar work is what keeps the tensor pipe waiting: no votes, no divisions, a wait
+    // per hand-over.
+    if (elect_one()) {
+      constexpr uint32_t IDESC_QK = idesc_bf16(BM, BN, 0, 0), IDESC_PV = idesc_bf16(BM, 128, 0, 1);
+      uint32_t kt = 0, pos = 0, nc = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // key tiles, ring, cleared, units, P tiles
+      bool ok = true;
+      // S = Q K^T of one tile; `at`: chunk where the keys begin
+      auto qk = [&](int i, uint32_t at, bool last) {
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
           const uint64_t a = desc_k(q_smem + (i * KC + c) * CHUNK), b = desc_k(ring + wrap<RING>(at + c) * CHUNK);
@@ -350,38 +354,73 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         tc_commit(pipe.bar(S_FULL + i));
         if (last) tc_commit(pipe.bar(Q_FREE + i));
-      }
-      __syncwarp();
-    };
-    // O += P V of one tile; keys: the sequence's keys from this key tile on
-    auto pv = [&](int i, uint32_t at, int j, int keys) -> bool {
+      };
+      // O += P V of one tile; keys: the sequence's keys from this key tile on
+      auto pv = [&](int i, uint32_t at, int j, int keys) -> bool {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t v = ring + wrap<RING>(at + h) * CHUNK;
-        if (!pipe.wait_warp(P_FULL + 2 * i + h, np[i] & 1u)) return false;
-        if (keys - h * 64 <= 0) continue;
-        if (keys - h * 64 < 64) {
-          // rows past the sequence's last key: cleared (a row is 128 bytes of each box; the
-          // swizzle stays inside it)
-          uint4* z = reinterpret_cast<uint4*>(gbase + (v - base));
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            for (int e = (keys - h * 64) * 8 + lane; e < 512; e += 32) z[q * 512 + e] = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_cta();
-          __syncwarp();
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t b = desc_v(v);
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t b = desc_v(ring + wrap<RING>(at + h) * CHUNK);
+          if (!pipe.wait(P_FULL + 2 * i + h, np[i] & 1u)) return false;
+          if (keys <= h * 64) continue;
+          tc_fence_after();
 #pragma unroll
           for (int s = 0; s < 4; ++s)
             mma_bf16_ts(t_o + i * BN, t_s + i * BN + h * 32 + s * 8, b + s * 128, IDESC_PV, j + h + s > 0);
         }
-        __syncwarp();
+        ++np[i];
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!(ok = pipe.wait(U_FULL + k % NS, (k / NS) & 1))) break;
+        const int4* w = reinterpret_cast<const int4*>(gbase + OFF_UNIT + (k % NS) * 32);
+        const int q0 = w[0].x, nk = w[0].w, n0 = w[1].z, n1 = w[1].w;
+        mbar_arrive(pipe.bar(U_FREE + k % NS));
+        if (q0 < 0) break;
+        const int all = max(n0, n1);
+        if (all == 0) continue;
+        if (!(ok = pipe.wait(K_FULL + kt % NO, (kt / NO) & 1u))) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = i ? n1 : n0;
+          if (ok && n > 0) {
+            if (!(ok = pipe.wait(Q_FULL + i, nu[i] & 1u))) continue;
+            tc_fence_after();
+            qk(i, pos, n == 1);
+            ++nu[i];
+          }
+        }
+        if (!ok) break;
+        tc_commit(pipe.bar(K_FREE + kt % NO));
+        for (int j = 0; j < all; ++j, ++kt) {
+          const uint32_t v_at = wrap<RING>(pos + KC), next = wrap<RING>(v_at + 2), o = kt % NO, o1 = (kt + 1) % NO;
+          const int keys = nk - j * BN;
+          if (j == max(all - 2, 0) && nk < all * BN) mbar_arrive(pipe.bar(V_GO));
+          if (!(ok = pipe.wait(V_FULL + o, (kt / NO) & 1u))) break;
+          if (keys < BN) {                                // its tail is being cleared
+            if (!(ok = pipe.wait(V_CLEAN, nc & 1u))) break;
+            ++nc;
+          }
+          if (j < n0 && !(ok = pv(0, v_at, j, keys))) break;
+          if (j + 1 < all && !(ok = pipe.wait(K_FULL + o1, ((kt + 1) / NO) & 1u))) break;
+          if (j + 1 < n0) qk(0, next, j + 2 == n0);
+          else if (j + 1 == n0) tc_commit(pipe.bar(O_DONE));
+          if (j < n1 && !(ok = pv(1, v_at, j, keys))) break;
+          tc_commit(pipe.bar(V_FREE + o));                // both tiles are past these values
+          if (j + 1 < n1) qk(1, next, j + 2 == n1);
+          else if (j + 1 == n1) tc_commit(pipe.bar(O_DONE + 1));
+          if (j + 1 < all) tc_commit(pipe.bar(K_FREE + o1));
+          pos = next;
+        }
       }
-      ++np[i];
-      return true;
-    };
+      tc_commit(pipe.bar(DRAIN));
+      pipe.drain(DRAIN, 0);                               // nothing in flight when TMEM is released
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ values past a sequence's last key
+    // They meet P = 0, but belong to another sequence or to nobody, and 0 x NaN is not 0.
+    uint32_t kt = 0, pos = 0, nc = 0;
+    bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
       const Unit u = read_unit(gbase, k);
@@ -390,45 +429,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (u.q0 < 0) break;
       const int all = max(u.n0, u.n1);
       if (all == 0) continue;
-      if (!(ok = pipe.wait_warp(K_FULL + kt % NO, (kt / NO) & 1u))) break;
-      for (int i = 0; i < 2 && ok; ++i)
-        if (u.tiles(i) > 0) {
-          if (!(ok = pipe.wait_warp(Q_FULL + i, nu[i] & 1u))) break;
-          tc_fence_after();
-          qk(i, pos, u.tiles(i) == 1);
-          ++nu[i];
+      const uint32_t last = kt + all - 1;
+      const int keys = u.nk - (all - 1) * BN;
+      if (keys < BN) {
+        const uint32_t at = (pos + (uint32_t)(all - 1) * (KC + 2) + KC) % RING;
+        // (not before the MMAs are close: the barrier's phases alternate)
+        if (!(ok = pipe.wait_warp(V_GO, nc & 1u))) break;
+        ++nc;
+        if (!(ok = pipe.wait_warp(V_FULL + last % NO, (last / NO) & 1u))) break;
+        // a row is 128 bytes of each 64-column box; the swizzle stays inside it
+        for (int h = 0; h < 2; ++h) {
+          uint4* z = reinterpret_cast<uint4*>(gbase + (ring - base) + wrap<RING>(at + h) * CHUNK);
+          const int from = max(keys - h * 64, 0);
+          if (keys <= h * 64) continue;                   // not multiplied at all
+          for (int e = from * 8 + lane; e < 512; e += 32) z[e] = z[512 + e] = make_uint4(0u, 0u, 0u, 0u);
         }
-      if (!ok) break;
-      if (elect_one()) tc_commit(pipe.bar(K_FREE + kt % NO));
-      __syncwarp();
-      for (int j = 0; j < all; ++j, ++kt) {
-        const uint32_t v_at = wrap<RING>(pos + KC), next = wrap<RING>(v_at + 2), o = kt % NO, o1 = (kt + 1) % NO;
-        if (!(ok = pipe.wait_warp(V_FULL + o, (kt / NO) & 1u))) break;
-        if (j < u.n0) {
-          if (!(ok = pv(0, v_at, j, u.nk - j * BN))) break;
-          if (j + 1 < all && !(ok = pipe.wait_warp(K_FULL + o1, ((kt + 1) / NO) & 1u))) break;
-          if (j + 1 < u.n0) qk(0, next, j + 2 == u.n0);
-          else if (elect_one()) tc_commit(pipe.bar(O_DONE));
-          __syncwarp();
-        } else if (j + 1 < all && !(ok = pipe.wait_warp(K_FULL + o1, ((kt + 1) / NO) & 1u))) {
-          break;
-        }
-        if (j < u.n1 && !(ok = pv(1, v_at, j, u.nk - j * BN))) break;
-        if (elect_one()) tc_commit(pipe.bar(V_FREE + o));       // both tiles are past these values
+        fence_proxy_async_cta();
         __syncwarp();
-        if (j < u.n1) {
-          if (j + 1 < u.n1) qk(1, next, j + 2 == u.n1);
-          else if (elect_one()) tc_commit(pipe.bar(O_DONE + 1));
-          __syncwarp();
-        }
-        if (j + 1 < all && elect_one()) tc_commit(pipe.bar(K_FREE + o1));
-        __syncwarp();
-        pos = next;
+        if (lane == 0) mbar_arrive(pipe.bar(V_CLEAN));
       }
+      kt += all;
+      pos = (pos + (uint32_t)all * (KC + 2)) % RING;
     }
-    if (elect_one()) tc_commit(pipe.bar(DRAIN));
-    __syncwarp();
-    pipe.drain(DRAIN, 0);                               // nothing in flight when TMEM is released
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax and output of one tile
     const int i = warp >> 2, r = threadIdx.x & 127;
