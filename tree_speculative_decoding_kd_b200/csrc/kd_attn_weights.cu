@@ -151,15 +151,6 @@ __device__ __forceinline__ int node_at(const Params& p, int b, int m) {
 
 __device__ __forceinline__ uint64_t desc_of(uint32_t saddr) { return smem_desc_sw128(saddr, 16, 1024); }
 
-// (d0, d1) = (a0, a1) * s + (c0, c1)
-__device__ __forceinline__ void ffma2v(float& d0, float& d1, float a0, float a1, float s, float c0, float c1) {
-  asm("{\n\t.reg .b64 ra, rs, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
-      "fma.rn.f32x2 rd, ra, rs, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(s), "f"(c0), "f"(c1));
-}
-
 // Adds exp2(s * scale + z) of four columns.
 __device__ __forceinline__ void add4(float (&acc)[4], const uint32_t* s, const float4& z, float scale) {
   float a, b, c, d;

@@ -116,6 +116,56 @@ __device__ __forceinline__ Unit read_unit(const uint8_t* gbase, int k) {
               uniform(b.x), uniform(b.y), uniform(b.z), uniform(b.w)};
 }
 
+// (a, b) = exp2 of both on the FMA pipe: x = i + f with i the nearest integer, 2^f by a
+// polynomial of degree 4 (minimax in relative error on [-1/2, 1/2], by the Remez exchange:
+// 2.6e-6), i added to the exponent bits.  Below -126 it gives 2^-126.
+__device__ __forceinline__ void exp2_poly2(float& a, float& b) {
+  constexpr float MAGIC = 12582912.f;                   // 1.5 x 2^23: adding it rounds to an integer
+  const float x = fmaxf(a, -126.f), y = fmaxf(b, -126.f);
+  float tx = x, ty = y;
+  fadd2(tx, ty, MAGIC, MAGIC);
+  float ix = tx, iy = ty;
+  fadd2(ix, iy, -MAGIC, -MAGIC);
+  float fx, fy;
+  ffma2v(fx, fy, ix, iy, -1.f, x, y);
+  float px, py;
+  ffma2(px, py, fx, fy, 0.009570102207362652f, 0.05591785907745361f);
+  fmul2add(px, py, px, py, fx, fy, 0.240247443318367f);
+  fmul2add(px, py, px, py, fx, fy, 0.6931217908859253f);
+  fmul2add(px, py, px, py, fx, fy, 0.9999992847442627f);
+  a = __uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23));
+  b = __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23));
+}
+
+// Pairs (of eight) whose exponentials the FMA pipe computes, the others go to the
+// special-function unit: sixteen a cycle and SM, it would be the tile's longest step alone.
+constexpr uint32_t POLY_PAIRS = 0x92;                   // 1, 4, 7
+
+// The first `n` columns of a half stay, the others become -inf.
+__device__ __forceinline__ void mask_half(uint32_t (&s)[64], int n) {
+#pragma unroll
+  for (int c = 0; c < 64; ++c) s[c] = c < n ? s[c] : 0xff800000u;
+}
+
+// P of one half of the keys: exponentials of s, rounded to bf16 in pk, summed up in (l0, l1).
+template <bool POLY>
+__device__ __forceinline__ void half_of_p(const uint32_t* s, uint32_t (&pk)[32], float scale, float nm, float& l0,
+                                          float& l1) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    float a, b;
+    ffma2(a, b, __uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), scale, nm);
+    if (POLY && (POLY_PAIRS >> (c & 7) & 1)) {
+      exp2_poly2(a, b);
+    } else {
+      a = ex2(a);
+      b = ex2(b);
+    }
+    fadd2(l0, l1, a, b);
+    pk[c] = pack_bf16x2(a, b);
+  }
+}
+
 // Asks the hardware for a block that has not started; the answer lands at `dst` and completes 16 bytes on `bar`.
 __device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
   asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
@@ -474,24 +524,29 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       for (int j = 0; j < n; ++j, ++ns) {
         if (!(ok = pipe.wait_warp(S_FULL + i, ns & 1u))) break;
         tc_fence_after();
-        uint32_t s[128];
+        const bool masked = (j + 1) * BN > lim0;        // some row of the tile does not see all of it
+        const int c0 = lim - j * BN;                    // columns this row sees
+        float mx;
+        {
+          uint32_t s[2][64];
+          tmem_ld64(s_at, s[0]);
+          tmem_ld64(s_at + 64, s[1]);
+          tmem_wait_ld();
+          if (masked) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, *reinterpret_cast<uint32_t(*)[32]>(s + q * 32));
-        tmem_wait_ld();
-        if ((j + 1) * BN > lim0) {                      // some row of the tile does not see all of it
-          const int c0 = lim - j * BN;
+            for (int h = 0; h < 2; ++h) mask_half(s[h], c0 - h * 64);
+          }
+          float mv[4];                                  // four chains: the latency of one would show
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = c < c0 ? s[c] : 0xff800000u;
+          for (int q = 0; q < 4; ++q) mv[q] = fmaxf(__uint_as_float(s[0][2 * q]), __uint_as_float(s[0][2 * q + 1]));
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mv[q] = fmax3(mv[q], __uint_as_float(s[c >> 6][(c & 63) + 2 * q]),
+                            __uint_as_float(s[c >> 6][(c & 63) + 2 * q + 1]));
+          mx = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
         }
-        float mv[4];                                    // four chains: the latency of one would show
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mv[q] = fmaxf(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1]));
-#pragma unroll
-        for (int c = 8; c < 128; c += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mv[q] = fmax3(mv[q], __uint_as_float(s[c + 2 * q]), __uint_as_float(s[c + 2 * q + 1]));
-        const float mx = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
         // the maximum in use moves when P would pass 2^8
         const bool rise = j == 0 || (mx - m) * p.scale_log2 > 8.f;
         if (j > 0 && __any_sync(0xffffffffu, rise)) {
@@ -521,15 +576,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float a, b;
-            ffma2(a, b, __uint_as_float(s[h * 64 + 2 * c]), __uint_as_float(s[h * 64 + 2 * c + 1]), p.scale_log2, nm);
-            a = ex2(a);
-            b = ex2(b);
-            fadd2(l0, l1, a, b);
-            pk[c] = pack_bf16x2(a, b);
+          // the scores once more: held over from the maximum, they would leave no registers to
+          // keep more than a few exponentials in flight
+          uint32_t s[64], pk[32];
+          tmem_ld64(s_at + h * 64, s);
+          tmem_wait_ld();
+          // (a masked score is -inf: its weight has to be 0, which only ex2 gives)
+          if (masked) {
+            mask_half(s, c0 - h * 64);
+            half_of_p<false>(s, pk, p.scale_log2, nm, l0, l1);
+          } else {
+            half_of_p<true>(s, pk, p.scale_log2, nm, l0, l1);
           }
           if (h == 1 && lane == 0 && (i == 0 ? j < both : j + 1 < both)) mbar_arrive(pipe.bar(my_turn));
           tmem_st32(s_at + h * 32, pk);
@@ -546,7 +603,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!(ok = pipe.wait_warp(O_DONE + i, nu & 1u))) break;
         ++nu;
         tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);       // a NaN sum stays one
+        const float inv = 1.f / l;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t o[32];
@@ -558,7 +615,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               uint32_t v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                v[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[c * 16 + 2 * e]) * inv,
+                v[e] = m == -INFINITY ? 0u : pack_bf16x2(__uint_as_float(o[c * 16 + 2 * e]) * inv,
                                                    __uint_as_float(o[c * 16 + 2 * e + 1]) * inv);
               st_global_v8(p.out + at * 128 + q * 32 + c * 16, v);
             }
@@ -568,7 +625,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       } else if (mine) {
         for (int c = 0; c < 16; ++c) st_global_v4(p.out + at * 128 + c * 8, 0u, 0u, 0u, 0u);
       }
-      if (mine) p.lse[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+      if (mine) p.lse[at] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
     }
   }
   tc_fence_before();
