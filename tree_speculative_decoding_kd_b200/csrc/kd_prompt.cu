@@ -61,8 +61,7 @@ enum Bar {
   O_DONE = P_FULL + 4,              // [2] the unit's last PV MMA of the tile is done
   U_FULL = O_DONE + 2,              // [NS] unit published
   U_FREE = U_FULL + NS,             // [NS] unit read (11 arrivals: a lane of each other warp)
-  TURN = U_FREE + NS,               // [2][4] a tile's warp has issued a key tile's exponentials
-  GO = TURN + 8,                    // the unit's last loads are near: time to claim the next one
+  GO = U_FREE + NS,                    // the unit's last loads are near: time to claim the next one
   CLC = GO + 1,                     // the next block's answer arrived
   DRAIN = CLC + 1,
   NBAR = DRAIN + 1
@@ -116,31 +115,6 @@ __device__ __forceinline__ Unit read_unit(const uint8_t* gbase, int k) {
               uniform(b.x), uniform(b.y), uniform(b.z), uniform(b.w)};
 }
 
-// (a, b) = exp2 of both on the FMA pipe: x = i + f with i the nearest integer, 2^f by a
-// polynomial of degree 4 (minimax in relative error on [-1/2, 1/2], by the Remez exchange:
-// 2.6e-6), i added to the exponent bits.  Below -126 it gives 2^-126.
-__device__ __forceinline__ void exp2_poly2(float& a, float& b) {
-  constexpr float MAGIC = 12582912.f;                   // 1.5 x 2^23: adding it rounds to an integer
-  const float x = fmaxf(a, -126.f), y = fmaxf(b, -126.f);
-  float tx = x, ty = y;
-  fadd2(tx, ty, MAGIC, MAGIC);
-  float ix = tx, iy = ty;
-  fadd2(ix, iy, -MAGIC, -MAGIC);
-  float fx, fy;
-  ffma2v(fx, fy, ix, iy, -1.f, x, y);
-  float px, py;
-  ffma2(px, py, fx, fy, 0.009570102207362652f, 0.05591785907745361f);
-  fmul2add(px, py, px, py, fx, fy, 0.240247443318367f);
-  fmul2add(px, py, px, py, fx, fy, 0.6931217908859253f);
-  fmul2add(px, py, px, py, fx, fy, 0.9999992847442627f);
-  a = __uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23));
-  b = __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23));
-}
-
-// Pairs (of eight) whose exponentials the FMA pipe computes, the others go to the
-// special-function unit: sixteen a cycle and SM, it would be the tile's longest step alone.
-constexpr uint32_t POLY_PAIRS = 0x92;                   // 1, 4, 7
-
 // The first `n` columns of a half stay, the others become -inf.
 __device__ __forceinline__ void mask_half(uint32_t (&s)[64], int n) {
 #pragma unroll
@@ -148,19 +122,14 @@ __device__ __forceinline__ void mask_half(uint32_t (&s)[64], int n) {
 }
 
 // P of one half of the keys: exponentials of s, rounded to bf16 in pk, summed up in (l0, l1).
-template <bool POLY>
 __device__ __forceinline__ void half_of_p(const uint32_t* s, uint32_t (&pk)[32], float scale, float nm, float& l0,
                                           float& l1) {
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
     float a, b;
     ffma2(a, b, __uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), scale, nm);
-    if (POLY && (POLY_PAIRS >> (c & 7) & 1)) {
-      exp2_poly2(a, b);
-    } else {
-      a = ex2(a);
-      b = ex2(b);
-    }
+    a = ex2(a);
+    b = ex2(b);
     fadd2(l0, l1, a, b);
     pk[c] = pack_bf16x2(a, b);
   }
@@ -506,8 +475,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int i = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = t_s + i * BN + lanes, o_at = t_o + i * BN + lanes;
-    const int my_turn = TURN + 4 * i + (warp & 3), other = TURN + 4 * (i ^ 1) + (warp & 3);
-    uint32_t ns = 0, nu = 0, nt = 0;                    // key tiles, units with work, turns waited for
+    uint32_t ns = 0, nu = 0;                            // key tiles, units with work
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = pipe.wait_warp(U_FULL + k % NS, (k / NS) & 1))) break;
@@ -515,7 +483,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
-      const int n = u.tiles(i), row = u.row + i * BM + r, both = min(u.n0, u.n1);
+      const int n = u.tiles(i), row = u.row + i * BM + r;
       // keys this row sees, and those the tile's first row does
       const int64_t off = (int64_t)u.nk - u.nq + 1;
       const int lim = (int)max((int64_t)0, min((int64_t)u.nk, row + off));
@@ -568,12 +536,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
         float l0 = 0.f, l1 = 0.f;
-        // the two tiles' warps of one scheduler take turns at the exponentials: tile 1 after
-        // tile 0 of the same key tile, tile 0 after tile 1 of the one before
-        if (j < both && (i == 1 || j > 0)) {
-          if (!(ok = pipe.wait_warp(other, nt & 1u))) break;
-          ++nt;
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           // the scores once more: held over from the maximum, they would leave no registers to
@@ -581,14 +543,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           uint32_t s[64], pk[32];
           tmem_ld64(s_at + h * 64, s);
           tmem_wait_ld();
-          // (a masked score is -inf: its weight has to be 0, which only ex2 gives)
-          if (masked) {
-            mask_half(s, c0 - h * 64);
-            half_of_p<false>(s, pk, p.scale_log2, nm, l0, l1);
-          } else {
-            half_of_p<true>(s, pk, p.scale_log2, nm, l0, l1);
-          }
-          if (h == 1 && lane == 0 && (i == 0 ? j < both : j + 1 < both)) mbar_arrive(pipe.bar(my_turn));
+          if (masked) mask_half(s, c0 - h * 64);
+          half_of_p(s, pk, p.scale_log2, nm, l0, l1);
           tmem_st32(s_at + h * 32, pk);
           tmem_wait_st();
           tc_fence_before();

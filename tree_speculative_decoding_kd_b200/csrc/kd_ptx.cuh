@@ -478,14 +478,6 @@ __device__ __forceinline__ void ffma2v(float& d0, float& d1, float a0, float a1,
       : "f"(a0), "f"(a1), "f"(s), "f"(c0), "f"(c1));
 }
 
-// (d0, d1) = (a0, a1) * (b0, b1) + (c, c)
-__device__ __forceinline__ void fmul2add(float& d0, float& d1, float a0, float a1, float b0, float b1, float c) {
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %6};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c));
-}
-
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
