@@ -115,17 +115,18 @@ __device__ __forceinline__ Unit read_unit(const uint8_t* gbase, int k) {
               uniform(b.x), uniform(b.y), uniform(b.z), uniform(b.w)};
 }
 
-// The first `n` columns of a half stay, the others become -inf.
-__device__ __forceinline__ void mask_half(uint32_t (&s)[64], int n) {
+// The first `n` of 32 columns stay, the others become -inf.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], int n) {
 #pragma unroll
-  for (int c = 0; c < 64; ++c) s[c] = c < n ? s[c] : 0xff800000u;
+  for (int c = 0; c < 32; ++c) s[c] = c < n ? s[c] : 0xff800000u;
 }
 
-// P of one half of the keys: exponentials of s, rounded to bf16 in pk, summed up in (l0, l1).
-__device__ __forceinline__ void half_of_p(const uint32_t* s, uint32_t (&pk)[32], float scale, float nm, float& l0,
-                                          float& l1) {
+// P of N columns: exponentials of s, rounded to bf16 in pk, summed up in (l0, l1).
+template <int N>
+__device__ __forceinline__ void exp_columns(const uint32_t (&s)[N], uint32_t (&pk)[N / 2], float scale, float nm,
+                                            float& l0, float& l1) {
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
+  for (int c = 0; c < N / 2; ++c) {
     float a, b;
     ffma2(a, b, __uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), scale, nm);
     a = ex2(a);
@@ -133,6 +134,20 @@ __device__ __forceinline__ void half_of_p(const uint32_t* s, uint32_t (&pk)[32],
     fadd2(l0, l1, a, b);
     pk[c] = pack_bf16x2(a, b);
   }
+}
+
+// Maximum of N columns, in four chains (the latency of one would show).
+template <int N>
+__device__ __forceinline__ float max_columns(const uint32_t* s) {
+  float mv[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) mv[q] = fmaxf(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1]));
+#pragma unroll
+  for (int c = 8; c < N; c += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      mv[q] = fmax3(mv[q], __uint_as_float(s[c + 2 * q]), __uint_as_float(s[c + 2 * q + 1]));
+  return fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
 }
 
 // Asks the hardware for a block that has not started; the answer lands at `dst` and completes 16 bytes on `bar`.
@@ -484,36 +499,35 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
       const int n = u.tiles(i), row = u.row + i * BM + r;
-      // keys this row sees, and those the tile's first row does
+      // keys this row sees, and the first and the last row of the warp
       const int64_t off = (int64_t)u.nk - u.nq + 1;
       const int lim = (int)max((int64_t)0, min((int64_t)u.nk, row + off));
-      const int lim0 = (int)max((int64_t)0, min((int64_t)u.nk, u.row + i * BM + off));
+      const int first = __shfl_sync(0xffffffffu, lim, 0), last = __shfl_sync(0xffffffffu, lim, 31);
       float m = -INFINITY, l = 0.f;                     // raw scores
       for (int j = 0; j < n; ++j, ++ns) {
         if (!(ok = pipe.wait_warp(S_FULL + i, ns & 1u))) break;
         tc_fence_after();
-        const bool masked = (j + 1) * BN > lim0;        // some row of the tile does not see all of it
-        const int c0 = lim - j * BN;                    // columns this row sees
-        float mx;
-        {
-          uint32_t s[2][64];
-          tmem_ld64(s_at, s[0]);
-          tmem_ld64(s_at + 64, s[1]);
-          tmem_wait_ld();
-          if (masked) {
+        // columns that every row of the warp sees, that some row does, and that this row does
+        const int c_all = first - j * BN, c_any = last - j * BN, c_row = lim - j * BN;
+        const bool whole = c_all >= BN;
+        float mx = -INFINITY;
+        if (whole) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) mask_half(s[h], c0 - h * 64);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[64];
+            tmem_ld64(s_at + h * 64, s);
+            tmem_wait_ld();
+            mx = fmaxf(mx, max_columns<64>(s));
           }
-          float mv[4];                                  // four chains: the latency of one would show
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mv[q] = fmaxf(__uint_as_float(s[0][2 * q]), __uint_as_float(s[0][2 * q + 1]));
-#pragma unroll
-          for (int c = 8; c < 128; c += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mv[q] = fmax3(mv[q], __uint_as_float(s[c >> 6][(c & 63) + 2 * q]),
-                            __uint_as_float(s[c >> 6][(c & 63) + 2 * q + 1]));
-          mx = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < min(BN, c_any); c += 32) {
+            uint32_t s[32];
+            tmem_ld32(s_at + c, s);
+            tmem_wait_ld();
+            if (c + 32 > c_all) mask32(s, c_row - c);
+            mx = fmaxf(mx, max_columns<32>(s));
+          }
         }
         // the maximum in use moves when P would pass 2^8
         const bool rise = j == 0 || (mx - m) * p.scale_log2 > 8.f;
@@ -536,19 +550,42 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         const float nm = m == -INFINITY ? 0.f : -m * p.scale_log2;
         float l0 = 0.f, l1 = 0.f;
+        // the scores are read once more: held over from the maximum, they would leave no
+        // registers to keep more than a few exponentials in flight
+        if (whole) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[64], pk[32];
+            tmem_ld64(s_at + h * 64, s);
+            tmem_wait_ld();
+            exp_columns<64>(s, pk, p.scale_log2, nm, l0, l1);
+            tmem_st32(s_at + h * 32, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(pipe.bar(P_FULL + 2 * i + h));
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t pk[16];
+            if (c < c_any) {
+              uint32_t s[32];
+              tmem_ld32(s_at + c, s);
+              tmem_wait_ld();
+              if (c + 32 > c_all) mask32(s, c_row - c);
+              exp_columns<32>(s, pk, p.scale_log2, nm, l0, l1);
+            } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // the scores once more: held over from the maximum, they would leave no registers to
-          // keep more than a few exponentials in flight
-          uint32_t s[64], pk[32];
-          tmem_ld64(s_at + h * 64, s);
-          tmem_wait_ld();
-          if (masked) mask_half(s, c0 - h * 64);
-          half_of_p(s, pk, p.scale_log2, nm, l0, l1);
-          tmem_st32(s_at + h * 32, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(pipe.bar(P_FULL + 2 * i + h));
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            }
+            tmem_st8(s_at + c / 2, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+            tmem_st8(s_at + c / 2 + 8, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+            if (c & 32) {
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(pipe.bar(P_FULL + 2 * i + (c >> 6)));
+            }
+          }
         }
         l += l0 + l1;
       }
@@ -571,7 +608,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               uint32_t v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                v[e] = m == -INFINITY ? 0u : pack_bf16x2(__uint_as_float(o[c * 16 + 2 * e]) * inv,
+                v[e] = lim == 0 ? 0u : pack_bf16x2(__uint_as_float(o[c * 16 + 2 * e]) * inv,
                                                    __uint_as_float(o[c * 16 + 2 * e + 1]) * inv);
               st_global_v8(p.out + at * 128 + q * 32 + c * 16, v);
             }
@@ -581,7 +618,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       } else if (mine) {
         for (int c = 0; c < 16; ++c) st_global_v4(p.out + at * 128 + c * 8, 0u, 0u, 0u, 0u);
       }
-      if (mine) p.lse[at] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
+      if (mine) p.lse[at] = lim == 0 ? -INFINITY : m * p.scale + logf(l);
     }
   }
   tc_fence_before();
