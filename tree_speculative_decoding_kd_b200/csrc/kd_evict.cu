@@ -1,13 +1,19 @@
 // Eviction by accumulated attention weight: a request's cache cut down to its first
 // `sink` slots, its last `recent` slots and the slots of the largest weights between.
 //
-// Two launches.  select_kernel (one CTA per request) finds the weight of the last slot
-// that is kept, by a radix selection over order-preserving 32-bit keys (11 + 11 + 10
-// bits, a histogram in shared memory each), and then walks the slots in order once,
-// numbering the kept ones: equal weights are taken from the lowest slot.  The move
-// copies the kept rows: bound by memory, 2 x 1152 bytes a row, 16 bytes per lane.
+// Two launches.  select_kernel (a cluster of up to 8 CTAs per request) finds the weight of
+// the last slot that is kept, by a radix selection over order-preserving 32-bit keys (11 +
+// 11 + 10 bits, a histogram in shared memory each, added up across the cluster through
+// distributed shared memory), and then walks the slots in order once, numbering the kept
+// ones: equal weights are taken from the lowest slot.  It is bound by latency: a dozen
+// dependent steps over a few KB.  One CTA per request took 66 us for 18 K slots and 34 us
+// for 32 K (the time is the histograms', which equal weights serialise).
+// The move copies the kept rows: bound by memory, 2 x 1152 bytes a row, 16 bytes per lane.
+// It is launched with the selection still running (programmatic dependent launch) and waits
+// for it on the device.
 
 #include "kd_common.cuh"
+#include "kd_ptx.cuh"
 #include "kd_slots.cuh"
 
 namespace kd {
@@ -16,6 +22,8 @@ namespace ev {
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int PER = 4;                       // neighbouring slots a thread numbers per step
+constexpr int CHUNK = THREADS * PER;         // slots a CTA works on per step
+constexpr int MAXC = 8;                      // CTAs of a cluster
 
 // Unsigned key in the order of the weights: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -56,11 +64,26 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
   return v + (w ? before : 0u);
 }
 
-__global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
-  __shared__ uint32_t hist[BINS];
+// A word of another CTA's shared memory.
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// CTA r of a cluster of cs takes the chunks r, r + cs, ... of its request's slots.
+__global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p, const int cs) {
+  __shared__ __align__(16) uint32_t hist[3][BINS];
   __shared__ uint32_t warp_sums[WARPS];
-  __shared__ uint32_t found[2];
-  const int b = blockIdx.x, tid = threadIdx.x;
+  __shared__ uint32_t found[2], totals[2];
+  asm volatile("griddepcontrol.launch_dependents;");      // the move may come up and wait
+  const int b = blockIdx.x / cs, tid = threadIdx.x;
+  const int rank = cs > 1 ? (int)ptx::cluster_ctarank() : 0;
   const int64_t L64 = p.lens[b];
   int32_t* kept = p.kept + (size_t)b * p.keep;
   const int64_t fit = L64 < p.keep ? L64 : p.keep;
@@ -74,35 +97,61 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       out |= !p.dst.pages_ok(b, q * p.dst.P, q * p.dst.P + 1);
     if (__syncthreads_or(out)) bad = KD_DEV_BAD_PAGE;
   }
-  if (bad) {
-    if (tid == 0) raise_dev_error(p.err, bad);
-    for (int m = tid; m < p.keep; m += THREADS) kept[m] = -1;
+  if (bad) {                                           // the same in every CTA of the cluster
+    if (rank == 0) {
+      if (tid == 0) raise_dev_error(p.err, bad);
+      for (int m = tid; m < p.keep; m += THREADS) kept[m] = -1;
+    }
     return;
   }
   const int L = (int)L64, first = p.sink, last = L - p.recent;
   const float* w = p.w_in + (int64_t)b * p.wi;
+  // a thread's PER neighbouring slots of a step; read once when one step covers the request
+  const int span = cs * CHUNK, j0 = rank * CHUNK + tid * PER, steps = (L + span - 1) / span;
+  float v[PER];
+  auto load = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = step * span + j0 + i;
+      v[i] = j < L ? w[j] : 0.f;
+    }
+  };
+  load(0);
   uint32_t thr = 0, need = 0;                          // keys above thr are kept, and `need` equal to it
-  if (L > p.keep) {
+  if (L > p.keep && p.keep > p.sink + p.recent) {
     need = (uint32_t)(p.keep - p.sink - p.recent);
+    for (int i = tid; i < 3 * BINS; i += THREADS) (&hist[0][0])[i] = 0u;
+    __syncthreads();
     uint32_t mask = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 3 && need; ++pass) {
+    for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < BINS; i += THREADS) hist[i] = 0u;
-      __syncthreads();
-      for (int j0 = first; j0 < last; j0 += THREADS) {
-        const int j = j0 + tid;
-        const uint32_t key = j < last ? order_key(w[j]) : 0u;
-        const bool in = j < last && (key & mask) == (thr & mask);
-        const uint32_t d = in ? (key >> shift) & digits : BINS;
-        // weights of one magnitude share a digit: one atomic per digit and warp
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        if (in && (tid & 31) == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
+#pragma unroll 1
+      for (int step = 0; step < steps; ++step) {
+        if (steps > 1) load(step);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int j = step * span + j0 + i;
+          const uint32_t key = order_key(v[i]);
+          if (j >= first && j < last && (key & mask) == thr) atomicAdd(&hist[pass][(key >> shift) & digits], 1u);
+        }
       }
-      __syncthreads();
+      if (cs > 1) {
+        __syncthreads();
+        ptx::cluster_sync();
+      } else {
+        __syncthreads();
+      }
       // thread t holds the bins 2047 - 2t and 2046 - 2t: sums run from the largest digit
-      const uint32_t h1 = hist[BINS - 1 - 2 * tid], h0 = hist[BINS - 2 - 2 * tid];
+      const uint32_t* mine = &hist[pass][BINS - 2 - 2 * tid];
+      uint32_t h0 = mine[0], h1 = mine[1];
+      for (int r = 1; r < cs; ++r) {                   // the others', from the next one on
+        const int q = rank + r < cs ? rank + r : rank + r - cs;
+        const uint2 o = ld_cluster_v2(ptx::map_to_rank(ptx::smem_u32(mine), (uint32_t)q));
+        h0 += o.x;
+        h1 += o.y;
+      }
       uint32_t total;
       const uint32_t upto = block_scan(h1 + h0, warp_sums, total), above = upto - h1 - h0;
       if (above < need && upto >= need) {
@@ -114,19 +163,19 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       thr |= found[0] << shift;
       need = found[1];
       mask |= digits << shift;
-      __syncthreads();
     }
   }
   const bool all = L <= p.keep, none = !all && p.keep == p.sink + p.recent;
   float* wo = p.w_out + (int64_t)b * p.wo;
   uint32_t taken = 0, equal = 0;                       // before this step: above or forced, and equal
-  for (int j0 = 0; j0 < L; j0 += THREADS * PER) {
-    float v[PER];
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    if (steps > 1) load(step);
+    const int at0 = step * span + j0;
     uint32_t kind[PER], mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int j = j0 + tid * PER + i;
-      v[i] = j < L ? w[j] : 0.f;
+      const int j = at0 + i;
       kind[i] = 0;
       if (j < L) {
         const uint32_t key = order_key(v[i]);
@@ -136,22 +185,44 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       mine += kind[i];
     }
     uint32_t total;
-    uint32_t at = block_scan(mine, warp_sums, total) - mine;   // all reads of this step are done
+    uint32_t at = block_scan(mine, warp_sums, total) - mine;
+    // every CTA has read its slots of this step before any weight is written (weights_out may
+    // be weights_in), and the ones before it say where its own numbers start
+    uint32_t before_t = 0, before_e = 0, all_t = total >> 16, all_e = total & 0xFFFFu;
+    if (cs > 1) {
+      if (tid == 0) totals[step & 1] = total;
+      __syncthreads();
+      ptx::cluster_sync();
+      for (int r = 0; r < cs; ++r) {
+        if (r == rank) continue;
+        const uint32_t o = ld_cluster_u32(ptx::map_to_rank(ptx::smem_u32(&totals[step & 1]), (uint32_t)r));
+        all_t += o >> 16;
+        all_e += o & 0xFFFFu;
+        if (r < rank) {
+          before_t += o >> 16;
+          before_e += o & 0xFFFFu;
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const uint32_t a = taken + (at >> 16), e = equal + (at & 0xFFFFu);
+      const uint32_t a = taken + before_t + (at >> 16), e = equal + before_e + (at & 0xFFFFu);
       if (kind[i] == 1u << 16 || (kind[i] == 1u && e < need)) {
         const uint32_t m = a + (e < need ? e : need);
-        kept[m] = j0 + tid * PER + i;
+        kept[m] = at0 + i;
         wo[m] = v[i];
       }
       at += kind[i];
     }
-    taken += total >> 16;
-    equal += total & 0xFFFFu;
+    taken += all_t;
+    equal += all_e;
   }
-  for (int m = (int)fit + tid; m < p.keep; m += THREADS) kept[m] = -1;
-  if (tid == 0) p.lens_out[b] = (int32_t)fit;
+  for (int m = (int)fit + rank * THREADS + tid; m < p.keep; m += cs * THREADS) kept[m] = -1;
+  if (cs > 1) {
+    __syncthreads();
+    ptx::cluster_sync();                               // nobody leaves while its memory is read
+  }
+  if (tid == 0 && rank == 0) p.lens_out[b] = (int32_t)fit;   // (lens_out may be cache_lens)
 }
 
 struct MoveParams {
@@ -168,6 +239,7 @@ constexpr int CC = KD_D_C / 8, CR = KD_D_R / 8;    // 16-byte pieces of a row
 constexpr int ROWS = 4;
 __global__ void __launch_bounds__(256) move_kernel(const MoveParams p) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection is complete
   const int m0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
   const int32_t* kept = p.kept + (size_t)b * p.keep;
   uint4 v[ROWS][2], x[ROWS];
@@ -204,6 +276,7 @@ __global__ void __launch_bounds__(512) move_inplace_kernel(const MoveParams p) {
   const bool lat = sl < CC / 4;
   uint4* base = lat ? p.cd + sl * 4 + piece : p.rd + (sl - CC / 4) * 4 + piece;
   const int64_t stride = lat ? p.dc : p.dr;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection is complete
   for (int m0 = 0; m0 < p.keep; m0 += 128 * STEP) {
     uint4 v[STEP];
     int s[STEP];
@@ -237,7 +310,7 @@ static int evict_impl(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc
       (int64_t)sink + recent > keep || src.cap > INT32_MAX || dst.cap > INT32_MAX || wi < src.cap ||
       wo < (dst.cap < keep ? dst.cap : keep) || (w_out == w_in && wi != wo))
     return KD_EINVAL;
-  int st = device_sms(nullptr);
+  int sms = 0, st = device_sms(&sms);
   if (st) return st;
   ev::SelectParams s;
   s.lens = cache_lens;
@@ -253,8 +326,20 @@ static int evict_impl(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc
   s.keep = keep;
   s.sink = sink;
   s.recent = recent;
-  ev::select_kernel<<<B, ev::THREADS, 0, stream>>>(s);
-  if ((st = launch_status("select_kernel"))) return st;
+  // CTAs for the longest request there can be, but no more than two per SM over all requests
+  int cs = 1;
+  while (cs < ev::MAXC && cs * (int64_t)ev::CHUNK < src.cap && 2 * cs * B <= 2 * sms) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  cfg.gridDim = dim3((unsigned)(B * cs));
+  cfg.blockDim = dim3(ev::THREADS);
+  cfg.stream = stream;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)cs;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if ((st = cuda_status(cudaLaunchKernelEx(&cfg, ev::select_kernel, s, cs), "select_kernel"))) return st;
   ev::MoveParams m;
   m.c = reinterpret_cast<const uint4*>(c_kv);
   m.r = reinterpret_cast<const uint4*>(k_rope);
@@ -268,11 +353,11 @@ static int evict_impl(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc
   m.dc = dc / 8;
   m.dr = dr / 8;
   m.keep = keep;
-  if (inplace)
-    ev::move_inplace_kernel<<<dim3(ev::SLICES, B), 512, 0, stream>>>(m);
-  else
-    ev::move_kernel<<<dim3((unsigned)((keep + 8 * ev::ROWS - 1) / (8 * ev::ROWS)), B), 256, 0, stream>>>(m);
-  return launch_status("move_kernel");
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = inplace ? dim3(ev::SLICES, B) : dim3((unsigned)((keep + 8 * ev::ROWS - 1) / (8 * ev::ROWS)), B);
+  cfg.blockDim = dim3(inplace ? 512 : 256);
+  return cuda_status(cudaLaunchKernelEx(&cfg, inplace ? ev::move_inplace_kernel : ev::move_kernel, m), "move_kernel");
 }
 
 // Whether the memory of two sets of rows (width elements each) meets.

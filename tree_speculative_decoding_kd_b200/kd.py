@@ -91,12 +91,17 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _stream_of(stream, device) -> int:
+    """_stream for the calls whose host time counts: the current stream's handle without a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
 def _need(t, dtype, name, contiguous=True):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     dts = dtype if isinstance(dtype, tuple) else (dtype,)
     if t.dtype not in dts:
@@ -381,44 +386,51 @@ def kd_kv_compact_paged(c_pages, r_pages, page_table, page_size, path, length, c
 
 
 # ------------------------------------------------------------------ operators next to the verify step
-def _on_device(*tensors):
-    """Every tensor given (None skipped) lies on the current CUDA device, whose stream runs the call."""
+def _on_device(*tensors) -> int:
+    """Index of the current CUDA device, on which every tensor given (None skipped) has to lie."""
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"tensor on cuda:{t.device.index}, the current device is cuda:{dev}")
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("every tensor must be a CUDA tensor")
+                if dev is not None:
+                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+                dev = d
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return dev
 
 
 def _typed(t, dtype, name, shape=None):
     """Contiguous tensor of `dtype` and, when given, of `shape`."""
-    if t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
 
 
-def _heads(t, name, heads=None, width=None):
-    """Token and head strides of a bf16 [tokens][heads][width] view (unit stride inside a head)."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.numel() and t.stride(2) != 1):
-        raise ValueError(f"{name} must be bf16 [tokens][heads][width], unit stride inside a head")
-    if (heads is not None and t.shape[1] != heads) or (width is not None and t.shape[2] != width):
-        raise ValueError(f"{name} must be [tokens][{heads}][{width}], is {tuple(t.shape)}")
-    if t.numel() == 0:
-        return 0, 0
-    return t.stride(0), t.stride(1)
+def _heads(t, name, tokens=None, heads=None, width=None):
+    """Shape and token and head strides of a bf16 [tokens][heads][width] view (unit stride inside a head)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bf16 [tokens][heads][width]")
+    T, H, D = t.shape
+    if (tokens is not None and T != tokens) or (heads is not None and H != heads) or (width is not None and D != width):
+        raise ValueError(f"{name} must be {[tokens, heads, width]} (None: any), is {[T, H, D]}")
+    if T == 0 or H == 0:
+        return T, H, D, 0, 0
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must have unit stride inside a head")
+    return T, H, D, st, sh
 
 
 def _rope_table(table, rot):
     _typed(table, torch.float32, "rope_table")
     if table.dim() != 2 or (rot is not None and table.shape[1] != rot):
         raise ValueError("rope_table must be [max_pos][rot]")
-    return table.shape[0], table.shape[1]
+    return table.shape
 
 
 def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, eps=1e-6, rot_offset=0,
@@ -427,35 +439,27 @@ def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, e
     None: no norm) and the rotation of its elements [rot_offset, rot_offset + rot) by
     positions [T] int32; rope_table fp32 [max_pos][rot], cos | sin.  Returns (q_out, k_out),
     allocated contiguous unless given; q_out=q, k_out=k works in place."""
-    _on_device(q, k, positions, rope_table, q_weight, k_weight, q_out, k_out, dev_error)
-    qt, qh = _heads(q, "q")
-    T, H, D = q.shape
+    dev = _on_device(q, k, positions, rope_table, q_weight, k_weight, q_out, k_out, dev_error)
+    T, H, D, qt, qh = _heads(q, "q")
     _typed(positions, torch.int32, "positions", (T,))
     max_pos, rot = _rope_table(rope_table, None)
     if q_weight is not None:
         _typed(q_weight, torch.bfloat16, "q_weight", (D,))
     if q_out is None:
         q_out = torch.empty(T, H, D, dtype=torch.bfloat16, device=q.device)
-    elif q_out.shape[0] != T:
-        raise ValueError("q_out must have q's shape")
-    qot, qoh = _heads(q_out, "q_out", H, D)
+    _, _, _, qot, qoh = _heads(q_out, "q_out", T, H, D)
     Hk = kt = kh = kot = koh = 0
     if k is not None:
-        Hk = k.shape[1] if k.dim() == 3 else 0
-        kt, kh = _heads(k, "k", Hk, D)
-        if k.shape[0] != T:
-            raise ValueError("q and k must have the same tokens")
+        _, Hk, _, kt, kh = _heads(k, "k", T, None, D)
         if k_weight is not None:
             _typed(k_weight, torch.bfloat16, "k_weight", (D,))
         if k_out is None:
             k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=q.device)
-        elif k_out.shape[0] != T:
-            raise ValueError("k_out must have k's shape")
-        kot, koh = _heads(k_out, "k_out", Hk, D)
-    _check(lib.kd_qk_norm_rope(_ptr(q), qt, qh, _ptr(k), kt, kh, _ptr(q_weight), _ptr(k_weight), eps,
-                               _ptr(rope_table), max_pos, _ptr(positions), T, H, Hk, D, rot, rot_offset,
-                               int(interleaved), _ptr(q_out), qot, qoh, _ptr(k_out), kot, koh, _ptr(dev_error),
-                               _stream(stream)), "kd_qk_norm_rope")
+        _, _, _, kot, koh = _heads(k_out, "k_out", T, Hk, D)
+    _check(lib.kd_qk_norm_rope(q.data_ptr(), qt, qh, _ptr(k), kt, kh, _ptr(q_weight), _ptr(k_weight), eps,
+                               rope_table.data_ptr(), max_pos, positions.data_ptr(), T, H, Hk, D, rot, rot_offset,
+                               interleaved, q_out.data_ptr(), qot, qoh, _ptr(k_out), kot, koh, _ptr(dev_error),
+                               _stream_of(stream, dev)), "kd_qk_norm_rope")
     return q_out, k_out
 
 
@@ -465,7 +469,7 @@ def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
         B = cache_lens.shape[0]
     if cache_lens.shape[0] != B:
         raise ValueError("cache_lens must be [B]")
-    if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != D_C + D_R or (kv.numel() and kv.stride(1) != 1):
+    if kv.dtype is not torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != D_C + D_R or kv.stride(1) != 1:
         raise ValueError("kv must be bf16 [T][576] with unit-stride rows")
     T = kv.shape[0]
     max_pos, _ = _rope_table(rope_table, D_R)
@@ -479,10 +483,7 @@ def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
         raise ValueError("without cu_seqlens the tokens must divide evenly among the requests")
     H = qt = qh = 0
     if q_rope_in is not None:
-        H = q_rope_in.shape[1] if q_rope_in.dim() == 3 else 0
-        qt, qh = _heads(q_rope_in, "q_rope_in", H, D_R)
-        if q_rope_in.shape[0] != T:
-            raise ValueError("q_rope_in must be [T][H][64]")
+        _, H, _, qt, qh = _heads(q_rope_in, "q_rope_in", T, None, D_R)
         if q_rope_out is None:
             q_rope_out = torch.empty(T, H, D_R, dtype=torch.bfloat16, device=kv.device)
         _typed(q_rope_out, torch.bfloat16, "q_rope_out", (T, H, D_R))
@@ -498,7 +499,7 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
     normed, the rope key rotated, both stored at slots cache_lens[b] + i; the queries' rope
     part q_rope_in [T][H][64] rotated beside them.  positions None: cache_lens[b] + i;
     cu_seqlens None: T / B tokens per request.  Returns q_rope_out (None without queries)."""
-    _on_device(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in, q_rope_out,
+    dev = _on_device(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in, q_rope_out,
                dev_error)
     sc, sr, cap = _cache_strides(c_kv, k_rope)
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
@@ -507,8 +508,8 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
         raise ValueError("the cache must hold B requests")
     _check(lib.kd_kv_norm_rope_write(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(kv), kv.stride(0),
                                      _ptr(kv_weight), eps, _ptr(rope_table), max_pos, _ptr(positions),
-                                     int(interleaved), _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H,
-                                     _ptr(q_rope_out), _ptr(dev_error), _stream(stream)), "kd_kv_norm_rope_write")
+                                     interleaved, _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H,
+                                     _ptr(q_rope_out), _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_norm_rope_write")
     return q_rope_out
 
 
@@ -516,7 +517,7 @@ def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_l
                                 cu_seqlens=None, B=None, kv_weight=None, eps=1e-6, interleaved=True, q_rope_in=None,
                                 q_rope_out=None, dev_error=None, stream=None):
     """kd_kv_norm_rope_write through a page table."""
-    _on_device(c_pages, r_pages, page_table, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in,
+    dev = _on_device(c_pages, r_pages, page_table, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in,
                q_rope_out, dev_error)
     sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
@@ -525,9 +526,9 @@ def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_l
         raise ValueError("page_table must be [B][pages per request]")
     _check(lib.kd_kv_norm_rope_write_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
                                            _ptr(cache_lens), _ptr(kv), kv.stride(0), _ptr(kv_weight), eps,
-                                           _ptr(rope_table), max_pos, _ptr(positions), int(interleaved),
+                                           _ptr(rope_table), max_pos, _ptr(positions), interleaved,
                                            _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H, _ptr(q_rope_out),
-                                           _ptr(dev_error), _stream(stream)), "kd_kv_norm_rope_write_paged")
+                                           _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_norm_rope_write_paged")
     return q_rope_out
 
 
@@ -539,25 +540,19 @@ def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu
     queries and of the keys (cu_seqlens_k when those differ: the queries are the last
     positions).  scale None: 1 / sqrt(192) with a rope part, else 1 / sqrt(128).
     Returns (out [T][H][128] bf16, lse [T][H] fp32)."""
-    _on_device(q_nope, k_nope, v, cu_seqlens_q, q_rope, k_rope, cu_seqlens_k, out, lse, dev_error)
-    qnt, qnh = _heads(q_nope, "q_nope", None, 128)
-    T, H, _ = q_nope.shape
-    knt, knh = _heads(k_nope, "k_nope", None, 128)
-    Tk, Hk, _ = k_nope.shape
-    vt, vh = _heads(v, "v", Hk, 128)
-    if v.shape[0] != Tk:
-        raise ValueError("k_nope and v must have the same tokens")
+    dev = _on_device(q_nope, k_nope, v, cu_seqlens_q, q_rope, k_rope, cu_seqlens_k, out, lse, dev_error)
+    T, H, _, qnt, qnh = _heads(q_nope, "q_nope", None, None, 128)
+    Tk, Hk, _, knt, knh = _heads(k_nope, "k_nope", None, None, 128)
+    _, _, _, vt, vh = _heads(v, "v", Tk, Hk, 128)
     if (q_rope is None) != (k_rope is None):
         raise ValueError("q_rope and k_rope go together")
     qrt = qrh = krt = krh = 0
     if q_rope is not None:
-        qrt, qrh = _heads(q_rope, "q_rope", H, D_R)
+        _, _, _, qrt, qrh = _heads(q_rope, "q_rope", T, H, D_R)
         if k_rope.dim() == 2:
-            krt, krh = _heads(k_rope.unsqueeze(1), "k_rope", 1, D_R)[0], 0
+            krt = _heads(k_rope.unsqueeze(1), "k_rope", Tk, 1, D_R)[3]
         else:
-            krt, krh = _heads(k_rope, "k_rope", Hk, D_R)
-        if q_rope.shape[0] != T or k_rope.shape[0] != Tk:
-            raise ValueError("q_rope and k_rope must have q_nope's and k_nope's tokens")
+            _, _, _, krt, krh = _heads(k_rope, "k_rope", Tk, Hk, D_R)
     _typed(cu_seqlens_q, torch.int32, "cu_seqlens_q")
     if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
         raise ValueError("cu_seqlens_q must be [B + 1]")
@@ -574,7 +569,7 @@ def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu
     _typed(lse, torch.float32, "lse", (T, H))
     _check(lib.kd_prompt_attn(_ptr(q_nope), qnt, qnh, _ptr(q_rope), qrt, qrh, _ptr(k_nope), knt, knh, _ptr(k_rope),
                               krt, krh, _ptr(v), vt, vh, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, T, Tk, H, Hk,
-                              scale, _ptr(out), _ptr(lse), _ptr(dev_error), _stream(stream)), "kd_prompt_attn")
+                              scale, _ptr(out), _ptr(lse), _ptr(dev_error), _stream_of(stream, dev)), "kd_prompt_attn")
     return out, lse
 
 
@@ -612,7 +607,7 @@ def kd_kv_attn_weights(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path=N
     kd_tree_accept; None: every node), added to weights_in [B][>= cap] fp32 (None: zeros).
     lse is kd_tree_verify_attn's.  Call it before kd_kv_compact: the new slots' weights are
     stored in compacted order.  Returns weights_out (weights_out=weights_in accumulates)."""
-    _on_device(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, dev_error)
+    dev = _on_device(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, dev_error)
     sc, sr, cap = _cache_strides(c_kv, k_rope)
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
                                                  weights_out, cap)
@@ -620,7 +615,7 @@ def kd_kv_attn_weights(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path=N
         raise ValueError("the cache must hold B requests")
     _check(lib.kd_kv_attn_weights(_ptr(q_abs), _ptr(q_rope), _ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens),
                                   _ptr(vis), _ptr(lse), _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
-                                  _ptr(weights_out), wo, _ptr(dev_error), _stream(stream)), "kd_kv_attn_weights")
+                                  _ptr(weights_out), wo, _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_attn_weights")
     return weights_out
 
 
@@ -628,7 +623,7 @@ def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_s
                              length=None, scale=1.0 / math.sqrt(192.0), weights_in=None, weights_out=None,
                              dev_error=None, stream=None):
     """kd_kv_attn_weights over a paged cache (page_size 64, 128 or 256)."""
-    _on_device(q_abs, q_rope, c_pages, r_pages, page_table, cache_lens, vis, lse, path, length, weights_in,
+    dev = _on_device(q_abs, q_rope, c_pages, r_pages, page_table, cache_lens, vis, lse, path, length, weights_in,
                weights_out, dev_error)
     sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
@@ -638,7 +633,7 @@ def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_s
     _check(lib.kd_kv_attn_weights_paged(_ptr(q_abs), _ptr(q_rope), _ptr(c_pages), _ptr(r_pages), sc, sr,
                                         int(page_size), _ptr(page_table), M, N, _ptr(cache_lens), _ptr(vis), _ptr(lse),
                                         _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
-                                        _ptr(weights_out), wo, _ptr(dev_error), _stream(stream)),
+                                        _ptr(weights_out), wo, _ptr(dev_error), _stream_of(stream, dev)),
            "kd_kv_attn_weights_paged")
     return weights_out
 
@@ -666,7 +661,7 @@ def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_
     and those of the largest weights between.  Without c_dst, r_dst it works in place (cache,
     cache_lens and weights_in are updated); with them the kept rows go to another cache.
     Returns (kept [B][keep] int32, weights_out, lens_out)."""
-    _on_device(c_kv, k_rope, cache_lens, weights_in, c_dst, r_dst, weights_out, lens_out, kept, dev_error)
+    dev = _on_device(c_kv, k_rope, cache_lens, weights_in, c_dst, r_dst, weights_out, lens_out, kept, dev_error)
     sc, sr, cap = _cache_strides(c_kv, k_rope)
     if (c_dst is None) != (r_dst is None):
         raise ValueError("c_dst and r_dst go together")
@@ -680,7 +675,7 @@ def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_
         raise ValueError("the caches must hold B requests")
     _check(lib.kd_kv_evict(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(weights_in), wi, int(keep),
                            int(sink), int(recent), B, _ptr(c_dst), _ptr(r_dst), dc, dr, dcap, _ptr(weights_out), wo,
-                           _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream(stream)), "kd_kv_evict")
+                           _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_evict")
     return kept, weights_out, lens_out
 
 
@@ -690,7 +685,7 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
     """kd_kv_evict through page tables: in place without dst_page_table (the request's tail
     pages are then free), else into the pages of dst_page_table (of c_dst, r_dst, or of the
     same pool), which must be none of the source's."""
-    _on_device(c_pages, r_pages, page_table, cache_lens, weights_in, c_dst, r_dst, dst_page_table, weights_out,
+    dev = _on_device(c_pages, r_pages, page_table, cache_lens, weights_in, c_dst, r_dst, dst_page_table, weights_out,
                lens_out, kept, dev_error)
     sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
     if (c_dst is None) != (r_dst is None) or (c_dst is not None and dst_page_table is None):
@@ -708,7 +703,7 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
     _check(lib.kd_kv_evict_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
                                  _ptr(cache_lens), _ptr(weights_in), wi, int(keep), int(sink), int(recent), B,
                                  _ptr(c_dst), _ptr(r_dst), dc, dr, _ptr(dst_page_table), DM, DN, _ptr(weights_out), wo,
-                                 _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream(stream)), "kd_kv_evict_paged")
+                                 _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_evict_paged")
     return kept, weights_out, lens_out
 
 
