@@ -5,13 +5,16 @@
 //   y = x / sqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos - b sin, a sin + b cos)
 //
 // Both are bound by memory (about 7 operations per 4 bytes moved), so every element is
-// read once and written once, 16 bytes at a time.  A head's D <= 256 elements lie in one
-// group of 8, 16 or 32 lanes, eight neighbouring elements per lane: the sum of squares
-// is a few shuffles inside the group, and the partner of a pair (i, i + rot/2) sits at
-// the same place of another lane, rot/16 lanes away.  A group takes four heads of one
-// token: four loads in flight per lane, and the token's cosines and sines, which cost
-// more loads than the data they turn, are read once for the four.  Sums, norm and
-// rotation are in fp32; the one rounding is the store's.
+// read once and written once, 16 bytes at a time.  A lane holds two pieces of eight
+// neighbouring elements of a head, chosen so that the rotation needs no other lane: with
+// pairs (i, i + rot/2) the two pieces are rot/2 apart.  (With one piece per lane the
+// rotation's shuffles, eight a piece, were what bounded the kernel: 75 us instead of the
+// figures below.)  A head's D <= 256 elements lie in a group of 4, 8 or 16 lanes; the sum
+// of squares is a few shuffles inside the group.  A group walks over some heads of one
+// token, so that the token's cosines and sines and the weights are read once for them; the
+// heads ahead are on their way into shared memory meanwhile (each lane copies and reads only
+// its own pieces: no barrier).  Sums, norm and rotation are in fp32; the one rounding is the
+// store's.
 
 #include "kd_common.cuh"
 #include "kd_ptx.cuh"
@@ -20,8 +23,23 @@
 namespace kd {
 namespace nr {
 
-constexpr int U = 4;                       // heads a group works on at once
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
+constexpr int DEPTH = 4;                   // heads on their way per group
+
+// A lane's ring of DEPTH heads, two 16-byte pieces each, in shared memory.
+struct Ring {
+  uint32_t at;                             // this lane's first piece; pieces of a block lie side by side
+  __device__ __forceinline__ explicit Ring(const uint4* smem) : at(ptx::smem_u32(smem + threadIdx.x)) {}
+  __device__ __forceinline__ uint32_t piece(int slot, int i) const { return at + (slot * 2 + i) * THREADS * 16; }
+  // Copies a piece (zeros when !on).
+  __device__ __forceinline__ void copy(int slot, int i, const void* src, bool on) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(piece(slot, i)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The oldest of the DEPTH groups on their way has landed.
+  __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+};
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -37,55 +55,38 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     ptx::pack_bf16x2(x[6], x[7]));
 }
 
-// One lane's part of a rotation: its eight elements start at element e of the rotated
-// range (or lie outside it: on == false).
+// One lane's part of a rotation: two pieces of eight elements, a and b.
 struct Turn {
-  float c[8], s[8];     // interleaved pairs use the first four
-  int partner;          // lane of the group that holds the pairs' other halves
+  float c[8], s[8];     // of the eight pairs (a_i, b_i); interleaved: four pairs of a, four of b
   bool on, inter;
-  // lane: this lane's index in its group; e: first element relative to the range
-  __device__ __forceinline__ void load(const float* row, int e, int rot, bool interleaved, int lane) {
-    on = e >= 0 && e < rot;
+  // ea, eb: first elements of the pieces relative to the rotated range, if both are in it
+  __device__ __forceinline__ void load(const float* row, int ea, int eb, int rot, bool rotated, bool interleaved) {
+    on = rotated;
     inter = interleaved;
-    partner = lane;
     if (!on) return;
-    const int half = rot >> 1;
-    if (inter) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + (e >> 1)));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + (e >> 1)));
-      c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-      s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
-      return;
-    }
-    const bool first = e < half;
-    const int i = first ? e : e - half;
-    partner = first ? lane + (half >> 3) : lane - (half >> 3);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + i + 4 * q));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + i + 4 * q));
-      c[4 * q] = a.x, c[4 * q + 1] = a.y, c[4 * q + 2] = a.z, c[4 * q + 3] = a.w;
-      const float sg = first ? -1.f : 1.f;
-      s[4 * q] = sg * b.x, s[4 * q + 1] = sg * b.y, s[4 * q + 2] = sg * b.z, s[4 * q + 3] = sg * b.w;
-    }
+    const float* sn = row + (rot >> 1);
+    const int i0 = inter ? ea >> 1 : ea, i1 = inter ? eb >> 1 : ea + 4;
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + i0)), c1 = __ldg(reinterpret_cast<const float4*>(row + i1));
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(sn + i0)), s1 = __ldg(reinterpret_cast<const float4*>(sn + i1));
+    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
   }
-  // All lanes of the warp call it; WIDTH: lanes of a group.
-  template <int WIDTH>
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
-    if (inter) {                                   // the same in every lane of the warp
-      if (!on) return;
+  __device__ __forceinline__ static void pair(float& x, float& y, float c, float s) {
+    const float a = x, b = y;
+    x = a * c - b * s;
+    y = a * s + b * c;
+  }
+  __device__ __forceinline__ void apply(float (&a)[8], float (&b)[8]) const {
+    if (!on) return;
+    if (inter) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * c[i] - b * s[i];
-        x[2 * i + 1] = a * s[i] + b * c[i];
+        pair(a[2 * i], a[2 * i + 1], c[i], s[i]);
+        pair(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = __shfl_sync(0xffffffffu, x[i], partner, WIDTH);
-      if (on) x[i] = x[i] * c[i] + p * s[i];
+      for (int i = 0; i < 8; ++i) pair(a[i], b[i], c[i], s[i]);
     }
   }
 };
@@ -96,7 +97,7 @@ struct QkSide {
   const uint16_t* w;
   uint16_t* out;
   int64_t it, ih, ot, oh;      // token and head strides, in and out
-  int heads, items;            // items = ceil(heads / U) groups per token
+  int heads, items;            // items = ceil(heads / per) groups per token
 };
 struct QkParams {
   QkSide q, k;
@@ -105,12 +106,16 @@ struct QkParams {
   int32_t* err;
   int64_t max_pos;
   float eps, inv_d;
-  int T, D, rot, off, inter;
+  int T, D, rot, off, inter, per;      // per: heads of a group
 };
 
-// G lanes per head (the least power of two that holds D / 8).
+// G lanes per head (the least power of two that holds D / 16).  Lane l of a group has
+//   l < rot / 16: elements off + 8 l and off + rot / 2 + 8 l, eight each: both halves of pairs;
+//   else: the elements outside the rotated range, sixteen in a row of those, the last lane maybe eight.
 template <int G>
 __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkParams p) {
+  __shared__ uint4 pieces[DEPTH * 2 * THREADS];
+  const Ring ring(pieces);
   const int lane = threadIdx.x & (G - 1);
   const unsigned items = (unsigned)(p.q.items + p.k.items);
   const unsigned g = blockIdx.x * (THREADS / G) + threadIdx.x / G;
@@ -126,38 +131,70 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkParams p)
   }
   const bool is_k = item >= (unsigned)p.q.items;
   const QkSide& s = is_k ? p.k : p.q;
-  const int h0 = (int)(is_k ? item - p.q.items : item) * U, e = lane * 8;
-  const bool mine = live && e < p.D;
-
-  uint4 raw[U];
-  const uint16_t* in = s.in + (int64_t)t * s.it + e;
+  const int h0 = (int)(is_k ? item - p.q.items : item) * p.per, n = live ? min(p.per, s.heads - h0) : 0;
+  const int rest = (p.D - p.rot) >> 3, r0 = 2 * (lane - (p.rot >> 4));     // pieces outside the range, this lane's first
+  const bool rotated = r0 < 0;
+  int ea, eb;
+  if (rotated) {
+    ea = p.off + 8 * lane;
+    eb = ea + (p.rot >> 1);
+  } else {
+    ea = 8 * r0 < p.off ? 8 * r0 : 8 * r0 + p.rot;
+    eb = 8 * (r0 + 1) < p.off ? 8 * (r0 + 1) : 8 * (r0 + 1) + p.rot;
+  }
+  const bool has_a = r0 < rest, has_b = rotated || r0 + 1 < rest;
+  const uint16_t* in = s.in + (int64_t)t * s.it + h0 * s.ih;
+  uint16_t* out = s.out + (int64_t)t * s.ot + h0 * s.oh;
+  auto ask = [&](int h) {
+    if (h < n) {
+      ring.copy(h & (DEPTH - 1), 0, in + (has_a ? h * s.ih + ea : 0), has_a);
+      ring.copy(h & (DEPTH - 1), 1, in + (has_b ? h * s.ih + eb : 0), has_b);
+    }
+    Ring::commit();
+  };
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    raw[u] = mine && h0 + u < s.heads ? *reinterpret_cast<const uint4*>(in + (h0 + u) * s.ih) : make_uint4(0, 0, 0, 0);
-  float w[8];
+  for (int h = 0; h < DEPTH; ++h) ask(h);
   const bool norm = s.w != nullptr;
-  if (norm && mine) unpack8(__ldg(reinterpret_cast<const uint4*>(s.w + e)), w);
+  float wa[8], wb[8];
+  if (norm && live) {
+    unpack8(has_a ? __ldg(reinterpret_cast<const uint4*>(s.w + ea)) : make_uint4(0, 0, 0, 0), wa);
+    unpack8(has_b ? __ldg(reinterpret_cast<const uint4*>(s.w + eb)) : make_uint4(0, 0, 0, 0), wb);
+  }
   Turn turn;
-  turn.load(p.table + (live ? at : 0) * p.rot, mine ? e - p.off : -1, p.rot, p.inter != 0, lane);
+  turn.load(p.table + at * p.rot, ea - p.off, eb - p.off, p.rot, live && rotated, p.inter != 0);
 
+  // the groups of a warp may have fewer heads or none: the shuffles are for all
+  const int most = __reduce_max_sync(0xffffffffu, n);
+#pragma unroll 1
+  for (int h = 0; h < most; ++h) {
+    Ring::wait();
+    float a[8], b[8];
+    unpack8(ptx::ld_shared_v4(ring.piece(h & (DEPTH - 1), 0)), a);
+    unpack8(ptx::ld_shared_v4(ring.piece(h & (DEPTH - 1), 1)), b);
+    ask(h + DEPTH);
+    float ss = 0.f, sb = 0.f;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float x[8];
-    unpack8(raw[u], x);
-    // the group's lanes agree on `norm`, a warp's groups may not: the shuffles are for all
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+    for (int i = 0; i < 8; ++i) {
+      ss += a[i] * a[i];
+      sb += b[i] * b[i];
+    }
+    ss += sb;
 #pragma unroll
     for (int m = G / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
     if (norm) {
       const float r = rsqrtf(ss * p.inv_d + p.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (mine ? w[i] : 0.f);
+      for (int i = 0; i < 8; ++i) {
+        a[i] = a[i] * r * wa[i];
+        b[i] = b[i] * r * wb[i];
+      }
     }
-    turn.template apply<G>(x);
-    if (mine && h0 + u < s.heads)
-      *reinterpret_cast<uint4*>(s.out + (int64_t)t * s.ot + (h0 + u) * s.oh + e) = pack8(x);
+    turn.apply(a, b);
+    if (h < n) {
+      if (has_a) *reinterpret_cast<uint4*>(out + ea) = pack8(a);
+      if (has_b) *reinterpret_cast<uint4*>(out + eb) = pack8(b);
+    }
+    out += s.oh;
   }
 }
 
@@ -171,7 +208,7 @@ struct WriteParams {
   SlotMap map;
   int64_t sc, sr, kv_stride, qt, qh, max_pos;
   float eps;
-  int B, T, n, H, items, inter;      // items = 1 + ceil(H / 16) warps per token
+  int B, T, n, H, items, inter, per;   // items = max(1, ceil(H / per)) warps per token
 };
 
 // Sequence of token t: the last b with cu[b] <= t (B when t lies past the last one).
@@ -185,9 +222,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
   return lo;
 }
 
-// One warp per item of a token: item 0 its latent and rope key, item 1 + i the rope parts
-// of query heads 16 i .. 16 i + 15 (eight lanes a head, four heads at a time).
+// One warp per item of a token: item i the rope parts of `per` query heads from per i on (four
+// lanes a head, eight heads at a time), item 0 the token's latent and rope key too, whose
+// loads are on their way with the queries' first ones.
 __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const WriteParams p) {
+  __shared__ uint4 pieces[DEPTH * 2 * THREADS];
+  const Ring ring(pieces);
   const int lane = threadIdx.x & 31;
   const unsigned wi = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
   const unsigned t = wi / (unsigned)p.items, item = wi - t * (unsigned)p.items;
@@ -215,67 +255,83 @@ __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const Write
   }
   const float* row = p.table + at * KD_D_R;
 
+  const int h0 = (int)item * p.per + (lane >> 2), end = min(p.H, (int)(item + 1) * p.per);
+  const int ea = (lane & 3) * 8, eb = ea + KD_D_R / 2;
+  const uint16_t* in = p.q_in + (int64_t)t * p.qt;
+  auto ask = [&](int i) {
+    const int h = h0 + 8 * i;
+    if (h < end) {
+      ring.copy(i & (DEPTH - 1), 0, in + h * p.qh + ea, true);
+      ring.copy(i & (DEPTH - 1), 1, in + h * p.qh + eb, true);
+    }
+    Ring::commit();
+  };
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) ask(i);
+
+  Turn turn;                                         // of the lane's two pieces of any head
   if (item == 0) {
-    if (L < 0 || L + count > p.map.cap) {
-      if (lane == 0) raise_dev_error(p.err, KD_DEV_CACHE_FULL);
-      return;
-    }
-    if (!p.map.pages_ok(b, slot, slot + 1)) {
-      if (lane == 0) raise_dev_error(p.err, KD_DEV_BAD_PAGE);
-      return;
-    }
     const uint16_t* src = p.kv + (int64_t)t * p.kv_stride;
-    uint4 raw[2], rr = make_uint4(0, 0, 0, 0);
+    uint4 raw[2], rr[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) raw[q] = *reinterpret_cast<const uint4*>(src + (lane + 32 * q) * 8);
-    if (lane < 8) rr = *reinterpret_cast<const uint4*>(src + KD_D_C + lane * 8);
-    Turn turn;
-    turn.load(row, lane < 8 ? lane * 8 : -1, KD_D_R, p.inter != 0, lane & 7);
-    float x[2][8], ss = 0.f;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      unpack8(raw[q], x[q]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[q][i] * x[q][i];
+    if (lane < 4) {
+      rr[0] = *reinterpret_cast<const uint4*>(src + KD_D_C + ea);
+      rr[1] = *reinterpret_cast<const uint4*>(src + KD_D_C + eb);
     }
-    const int64_t r = p.map.row(b, slot);
-    if (p.w) {
-#pragma unroll
-      for (int m = 16; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      const float rs = rsqrtf(ss * (1.f / KD_D_C) + p.eps);
+    turn.load(row, ea, eb, KD_D_R, true, p.inter != 0);
+    int bad = 0;
+    if (L < 0 || L + count > p.map.cap) bad = KD_DEV_CACHE_FULL;
+    else if (!p.map.pages_ok(b, slot, slot + 1)) bad = KD_DEV_BAD_PAGE;
+    if (bad) {
+      if (lane == 0) raise_dev_error(p.err, bad);
+    } else {
+      const int64_t r = p.map.row(b, slot);
+      float x[2][8], ss = 0.f;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        float w[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.w + (lane + 32 * q) * 8)), w);
+        unpack8(raw[q], x[q]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[q][i] = x[q][i] * rs * w[i];
+        for (int i = 0; i < 8; ++i) ss += x[q][i] * x[q][i];
+      }
+      if (p.w) {
+#pragma unroll
+        for (int m = 16; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float rs = rsqrtf(ss * (1.f / KD_D_C) + p.eps);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float w[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(p.w + (lane + 32 * q) * 8)), w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[q][i] = x[q][i] * rs * w[i];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<uint4*>(p.c_kv + r * p.sc + (lane + 32 * q) * 8) = pack8(x[q]);
+      if (lane < 4) {
+        unpack8(rr[0], x[0]);
+        unpack8(rr[1], x[1]);
+        turn.apply(x[0], x[1]);
+        *reinterpret_cast<uint4*>(p.k_rope + r * p.sr + ea) = pack8(x[0]);
+        *reinterpret_cast<uint4*>(p.k_rope + r * p.sr + eb) = pack8(x[1]);
       }
     }
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      *reinterpret_cast<uint4*>(p.c_kv + r * p.sc + (lane + 32 * q) * 8) = pack8(x[q]);
-    float y[8];
-    unpack8(rr, y);
-    turn.template apply<8>(y);
-    if (lane < 8) *reinterpret_cast<uint4*>(p.k_rope + r * p.sr + lane * 8) = pack8(y);
-    return;
+  } else {
+    turn.load(row, ea, eb, KD_D_R, true, p.inter != 0);
   }
 
-  const int h0 = (int)(item - 1) * 16 + (lane >> 3), e = (lane & 7) * 8;
-  uint4 raw[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    raw[u] = h0 + 4 * u < p.H ? *reinterpret_cast<const uint4*>(p.q_in + (int64_t)t * p.qt + (h0 + 4 * u) * p.qh + e)
-                              : make_uint4(0, 0, 0, 0);
-  Turn turn;
-  turn.load(row, e, KD_D_R, p.inter != 0, lane & 7);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float x[8];
-    unpack8(raw[u], x);
-    turn.template apply<8>(x);
-    if (h0 + 4 * u < p.H)
-      *reinterpret_cast<uint4*>(p.q_out + ((int64_t)t * p.H + h0 + 4 * u) * KD_D_R + e) = pack8(x);
+  uint16_t* out = p.q_out + ((int64_t)t * p.H + h0) * KD_D_R;
+#pragma unroll 1
+  for (int i = 0; h0 + 8 * i < end; ++i, out += 8 * KD_D_R) {
+    Ring::wait();
+    float a[8], b[8];
+    unpack8(ptx::ld_shared_v4(ring.piece(i & (DEPTH - 1), 0)), a);
+    unpack8(ptx::ld_shared_v4(ring.piece(i & (DEPTH - 1), 1)), b);
+    ask(i + DEPTH);
+    turn.apply(a, b);
+    *reinterpret_cast<uint4*>(out + ea) = pack8(a);
+    *reinterpret_cast<uint4*>(out + eb) = pack8(b);
   }
 }
 
@@ -303,11 +359,16 @@ extern "C" int kd_qk_norm_rope(const kd_bf16_t* q, int64_t qt, int64_t qh, const
     return KD_EINVAL;
   if (Hk && (!k || !k_out || !aligned16(k) || !aligned16(k_out) || !strides_ok(kt, kh) || !strides_ok(kot, koh)))
     return KD_EINVAL;
-  int st = device_sms(nullptr);
+  int sms = 0, st = device_sms(&sms);
   if (st) return st;
+  const int G = D <= 64 ? 4 : D <= 128 ? 8 : 16;
+  // heads of a group: as many as leave every SM about 1024 lanes of work, at most 8
+  int per = 8;
+  while (per > 1 && (int64_t)T * ((H + per - 1) / per + (Hk + per - 1) / per) * G < (int64_t)sms * 1024) per /= 2;
   nr::QkParams p;
-  p.q = {q, q_weight, q_out, qt, qh, qot, qoh, H, (H + nr::U - 1) / nr::U};
-  p.k = {k, k_weight, k_out, kt, kh, kot, koh, Hk, (Hk + nr::U - 1) / nr::U};
+  p.per = per;
+  p.q = {q, q_weight, q_out, qt, qh, qot, qoh, H, (H + per - 1) / per};
+  p.k = {k, k_weight, k_out, kt, kh, kot, koh, Hk, (Hk + per - 1) / per};
   p.table = rope_table;
   p.pos = positions;
   p.err = dev_error;
@@ -319,12 +380,11 @@ extern "C" int kd_qk_norm_rope(const kd_bf16_t* q, int64_t qt, int64_t qh, const
   p.rot = rot;
   p.off = rot_offset;
   p.inter = interleaved;
-  const int G = D <= 64 ? 8 : D <= 128 ? 16 : 32;
   const int64_t groups = (int64_t)T * (p.q.items + p.k.items);
   const unsigned grid = (unsigned)((groups * G + nr::THREADS - 1) / nr::THREADS);
-  if (G == 8) nr::qk_norm_rope_kernel<8><<<grid, nr::THREADS, 0, stream>>>(p);
-  else if (G == 16) nr::qk_norm_rope_kernel<16><<<grid, nr::THREADS, 0, stream>>>(p);
-  else nr::qk_norm_rope_kernel<32><<<grid, nr::THREADS, 0, stream>>>(p);
+  if (G == 4) nr::qk_norm_rope_kernel<4><<<grid, nr::THREADS, 0, stream>>>(p);
+  else if (G == 8) nr::qk_norm_rope_kernel<8><<<grid, nr::THREADS, 0, stream>>>(p);
+  else nr::qk_norm_rope_kernel<16><<<grid, nr::THREADS, 0, stream>>>(p);
   return launch_status("qk_norm_rope_kernel");
 }
 
@@ -341,7 +401,7 @@ static int write_impl(kd_bf16_t* c_kv, kd_bf16_t* k_rope, int64_t sc, int64_t sr
       !rope_table || !aligned16(rope_table))
     return KD_EINVAL;
   if (H && (!q_in || !q_out || !aligned16(q_in) || !aligned16(q_out) || !strides_ok(qt, qh))) return KD_EINVAL;
-  int st = device_sms(nullptr);
+  int sms = 0, st = device_sms(&sms);
   if (st) return st;
   nr::WriteParams p;
   p.c_kv = c_kv;
@@ -367,7 +427,10 @@ static int write_impl(kd_bf16_t* c_kv, kd_bf16_t* k_rope, int64_t sc, int64_t sr
   p.T = T;
   p.n = cu ? 0 : T / B;
   p.H = H;
-  p.items = 1 + (H + 15) / 16;
+  // query heads of a warp: as many as leave every SM about 32 warps of work, 8 to 64
+  p.per = 64;
+  while (p.per > 8 && (int64_t)T * ((H + p.per - 1) / p.per) < (int64_t)sms * 32) p.per /= 2;
+  p.items = H > p.per ? (H + p.per - 1) / p.per : 1;
   p.inter = interleaved;
   const unsigned grid = (unsigned)(((int64_t)T * p.items + nr::THREADS / 32 - 1) / (nr::THREADS / 32));
   nr::kv_norm_rope_write_kernel<<<grid, nr::THREADS, 0, stream>>>(p);
