@@ -2,28 +2,33 @@
 // TMA):
 //   col_j = sum over counted rows (node i, head h) that see slot j of exp(s_ihj - lse_ih).
 //
-// The scores are computed transposed, S^T = K Q^T: 128 keys are the M rows of the MMA (the
-// TMEM lanes), up to 256 query rows its N columns.  A thread of the epilogue then owns one
-// key and adds up along its own columns: no reduction between threads, no second product,
-// a fixed order.  With the rows' lse known, one pass is enough: nothing runs a maximum.
+// The scores are computed transposed, S^T = K Q^T: keys are the M rows of the MMA (the TMEM
+// lanes), up to 256 query rows its N columns.  A thread of the epilogue then owns one key
+// and adds up along its own columns: no reduction between threads, no second product, a
+// fixed order.  With the rows' lse known, one pass is enough: nothing runs a maximum.
 //
-// A unit is (request, 128 keys); a cluster of 1, 2, 4 or 8 CTAs shares a unit by dealing
-// the query tiles out among its CTAs, whose sums meet in the first CTA's shared memory.
-// Per CTA, K (128 keys x 576, nine 16 KB chunks of 64 columns) stays in shared memory for
-// the unit; Q streams past it from L2 through a ring of 32 KB stages (256 rows x 64
-// columns).  A K chunk is refilled for the next unit as soon as the last query tile has
-// used it, so that with few rows (one query tile: bound by the cache's bytes) the next
-// unit's keys stream in behind the current one's products.
+// Two CTAs work as a pair (cta_group::2): M = 256 keys, 128 in each CTA's shared memory
+// (nine 16 KB chunks of 64 columns, there for the unit), while each CTA holds only half of
+// the query rows of a chunk.  The query rows stream past the keys from L2 at 32 bytes a
+// cycle and SM, half of what one CTA alone would need for the tensor pipe's rate, and the
+// 64 KB that are left for them hold four stages instead of two.  (Alone, a CTA with two
+// 32 KB stages waited for L2: 588 us for 4 x 16384 keys and 8192 rows, 195 us for the
+// accepted paths of 64 requests.)  A K chunk is refilled for the next unit as soon as the
+// last query tile has used it, so that with few rows (one query tile: bound by the cache's
+// bytes) the next unit's keys stream in behind the current one's products.
+//
+// A unit is (request, 256 keys); a cluster of 1, 2 or 4 pairs shares a unit by dealing the
+// query tiles out among its pairs, whose sums meet in the first pair's shared memory.
 //
 // Query tiles hold whole nodes: rows of one node are contiguous in memory, nodes on an
 // accepted path are not, so a stage is filled by one box per node, 16-row aligned (rows
 // that pad a node up are zeroed once and get lse = inf).  When every node counts and H is a
 // multiple of 16, one box fills the stage.
 //
-// Roles: warp 0 loads K, warp 1 loads Q, warp 2 issues the MMAs, warp 3 stages the rows'
-// lse and masks, warps 4 to 11 are the epilogue (two groups of four warps, taking the S
-// tile's 32-column chunks in turn).  Two S tiles of 256 TMEM columns alternate.  Every wait
-// is bounded (kd_pipe.cuh).  No TMA multicast.
+// Roles in each CTA: warp 0 loads K, warp 1 loads Q, warp 2 (one thread, even CTA) issues the
+// MMAs, warp 3 stages the rows' lse and masks, warps 4 to 11 are the epilogue (two groups of
+// four warps, taking the S tile's 32-column chunks in turn).  Two S tiles of 256 TMEM columns
+// alternate.  Every wait is bounded (kd_pipe.cuh).  No TMA multicast.
 
 #include <math.h>
 
@@ -39,25 +44,27 @@ namespace aw {
 using namespace ptx;
 
 constexpr int THREADS = 384;
-constexpr int BK = 128;                       // keys per unit
+constexpr int BK = 128;                       // keys per CTA
+constexpr int UK = 2 * BK;                    // keys per unit
 constexpr int BN = 256;                       // query rows per tile
 constexpr int NCH = 9;                        // 64-column chunks: 8 latent, 1 rope
 constexpr int KCHUNK = BK * 128;              // bytes
-constexpr int QSTAGE = BN * 128;
-constexpr int NQ = 2;                         // Q ring stages
+constexpr int QSTAGE = BN / 2 * 128;          // a CTA's half of the rows
+constexpr int NQ = 4;                         // Q ring stages
 constexpr int NS = 2;                         // S tiles in TMEM
-constexpr int MAXC = 8;                       // CTAs of a cluster
+constexpr int MAXP = 4;                       // pairs of a cluster
 
 enum Bar {
-  K_FULL = 0,                   // chunk landed (TMA)
-  K_FREE = K_FULL + NCH,        // chunk used for the last time in its unit (MMA commit)
-  Q_FULL = K_FREE + NCH,
-  Q_FREE = Q_FULL + NQ,
+  K_FULL = 0,                   // even CTA: both CTAs' chunk landed (TMA)
+  K_FREE = K_FULL + NCH,        // chunk used for the last time in its unit (MMA commit, both CTAs)
+  Q_FULL = K_FREE + NCH,        // even CTA: both halves landed
+  Q_FREE = Q_FULL + NQ,         // stage used (both CTAs)
   Z_FULL = Q_FREE + NQ,         // lse and masks of the tile staged (32 arrivals)
-  S_FULL = Z_FULL + NS,
-  S_FREE = S_FULL + NS,         // S tile and its lse read (256 arrivals)
-  P_FULL = S_FREE + NS,         // first CTA: the others' sums of a unit arrived
-  P_FREE = P_FULL + 2,          // other CTAs: the first has read them
+  Z_FREE = Z_FULL + NS,         // the epilogue has read them (8 arrivals: a lane of each warp)
+  S_FULL = Z_FREE + NS,         // S tile ready (both CTAs)
+  S_FREE = S_FULL + NS,         // even CTA: S tile read in both CTAs (16 arrivals)
+  P_FULL = S_FREE + NS,         // first pair: the others' sums of a unit arrived
+  P_FREE = P_FULL + 2,          // other pairs: the first has read them
   DRAIN = P_FREE + 2,           // all MMAs done
   NBAR = DRAIN + 1
 };
@@ -66,8 +73,8 @@ constexpr int OFF_Z = 1024;                             // f32 [NS][256]: -lse l
 constexpr int OFF_NODE = OFF_Z + NS * BN * 4;           // u8 [NS][256]: node of each column
 constexpr int OFF_VIS = OFF_NODE + NS * BN;             // u32 [NS][128][4]: masks of the tile's nodes, by place in the tile
 constexpr int OFF_X = OFF_VIS + NS * 128 * 16;          // f32 [2][128]: sums of the second group
-constexpr int OFF_PART = OFF_X + 2 * BK * 4;            // f32 [2][MAXC - 1][128]: sums of the other CTAs
-constexpr int OFF_K = ((OFF_PART + 2 * (MAXC - 1) * BK * 4 + 1023) / 1024) * 1024;
+constexpr int OFF_PART = OFF_X + 2 * BK * 4;            // f32 [2][MAXP - 1][128]: sums of the other pairs
+constexpr int OFF_K = ((OFF_PART + 2 * (MAXP - 1) * BK * 4 + 1023) / 1024) * 1024;
 constexpr int OFF_Q = OFF_K + NCH * KCHUNK;
 constexpr int SMEM = OFF_Q + NQ * QSTAGE + 1024;
 static_assert(NBAR * 8 <= OFF_ABORT && SMEM <= 232448, "shared memory");
@@ -80,7 +87,7 @@ struct Params {
   int32_t* err;
   int64_t cap, wi, wo, pages;
   int B, n, H, W, P, M;         // page size (0: contiguous) and pages per request
-  int Hp, per_tile;             // rows a node takes in a tile, nodes per tile
+  int Hp, per_tile;             // rows a node takes in a tile, nodes per tile (even)
   int linear;                   // one box per stage: `linear` rows (0: a box per node)
   int kbox;                     // rows of a K box
   float scale_log2;
@@ -99,7 +106,7 @@ struct Cursor {
     if (L < 0 || L + p.n > p.cap) return 1;             // one unit that reports it
     const int c = p.path ? p.len[b] : p.n;
     if (c < 1 || c > p.n) return 1;
-    return (int)((L + p.n + BK - 1) / BK);
+    return (int)((L + p.n + UK - 1) / UK);
   }
   __device__ __forceinline__ void window(const Params& p, int first) {
     b0 = first;
@@ -163,15 +170,17 @@ __device__ __forceinline__ void add4(float (&acc)[4], const uint32_t* s, const f
 __global__ void __launch_bounds__(THREADS, 1)
 weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant__ CUtensorMap tm_qr,
                const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_r, const Params p,
-               const int csize) {
+               const int pairs) {
   extern __shared__ uint8_t dyn[];
   uint8_t* gbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
   const uint32_t base = smem_u32(gbase);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = csize > 1 ? (int)cluster_ctarank() : 0;
-  const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), half = rank & 1, pr = rank >> 1;
+  const int cluster = blockIdx.x / (2 * pairs), clusters = gridDim.x / (2 * pairs);
+  const uint16_t both = (uint16_t)(3u << (rank & ~1));
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
   const Pipe pipe{base, abort_flag, p.err};
+  auto even = [&](int bar) { return map_to_rank(pipe.bar(bar), (uint32_t)(rank & ~1)); };
 
   // the rows that pad a node stay zero: no box ever writes them
   for (int i = threadIdx.x; i < NQ * QSTAGE / 16; i += THREADS)
@@ -179,16 +188,16 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     for (int i = 0; i < NBAR; ++i) {
-      const bool z = i >= Z_FULL && i < Z_FULL + NS, s = i >= S_FREE && i < S_FREE + NS;
-      const bool pf = i >= P_FULL && i < P_FULL + 2;
-      mbar_init(base + 8 * i, z ? 32 : s ? 256 : pf ? (csize > 1 ? 128 * (csize - 1) : 1) : 1);
+      const int n = i >= Z_FULL && i < Z_FULL + NS ? 32 : i >= Z_FREE && i < Z_FREE + NS ? 8
+                    : i >= S_FREE && i < S_FREE + NS ? 16 : i >= P_FULL && i < P_FULL + 2 && pairs > 1 ? 128 * (pairs - 1) : 1;
+      mbar_init(base + 8 * i, n);
     }
     fence_mbar_init();
   }
   fence_proxy_async_cta();
   if (warp == 3) {
-    tmem_alloc(base + OFF_TMEM, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(base + OFF_TMEM, 512);
+    tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_qa);
@@ -198,9 +207,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
-  if (csize > 1) cluster_sync();                        // barriers of all CTAs are ready
+  cluster_sync();                                       // barriers of all CTAs are ready
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM), 0);
 
   Cursor cur;
   int bad;
@@ -211,12 +220,12 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
     uint32_t it = 0;                                    // units loaded
     bool ok = true;
     while (ok && cur.next(p, bad)) {
-      if (bad || rank >= cur.tiles) continue;
+      if (bad || pr >= cur.tiles) continue;
       int64_t row[2];
       const int boxes = BK / p.kbox;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t key = (int64_t)cur.kt * BK + i * p.kbox;
+        const int64_t key = (int64_t)cur.kt * UK + half * BK + i * p.kbox;
         if (!p.P) row[i] = (int64_t)cur.b * p.cap + key;
         else {
           const int64_t q = key / p.P;                  // pages past the last one, or bad ones: page 0
@@ -228,19 +237,20 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
       for (; c < NCH; ++c) {
         if (!(ok = pipe.wait_warp(K_FREE + c, (it & 1u) ^ 1u))) break;
         if (lane == 0) {
-          const uint32_t bar = pipe.bar(K_FULL + c);
-          mbar_arrive_expect_tx(bar, KCHUNK);
+          const uint32_t bar = even(K_FULL + c);
+          if (half == 0) mbar_arrive_expect_tx(pipe.bar(K_FULL + c), 2 * KCHUNK);
           for (int i = 0; i < boxes; ++i)
-            tma_load_3d(base + OFF_K + c * KCHUNK + i * p.kbox * 128, c < 8 ? &tm_c : &tm_r, c < 8 ? c * 64 : 0,
-                        (int32_t)row[i], 0, bar);
+            tma_load_3d_pair(base + OFF_K + c * KCHUNK + i * p.kbox * 128, c < 8 ? &tm_c : &tm_r, c < 8 ? c * 64 : 0,
+                             (int32_t)row[i], 0, bar);
         }
         __syncwarp();
       }
       if (ok) ++it;
-      else
+      else if (half == 0)
         while (c-- > 0) pipe.drain(K_FULL + c, it & 1u);  // chunks of this unit that were asked for
     }
-    if (it > 0)
+    // (the odd CTA's copies land on the even CTA's barriers; neither leaves before the other)
+    if (it > 0 && half == 0)
       for (int c = 0; c < NCH; ++c) pipe.drain(K_FULL + c, (it - 1) & 1u);
   } else if (warp == 1) {
     // ------------------------------------------------------------ Q
@@ -248,60 +258,68 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
     bool ok = true;
     while (ok && cur.next(p, bad)) {
       if (bad) continue;
-      for (int t = rank; t < cur.tiles && ok; t += csize) {
-        const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0);
-        // lane i loads the box of node m0 + i (+ 32, ...): rows of the flat [B n H] query
+      for (int t = pr; t < cur.tiles && ok; t += pairs) {
+        const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0), first = half * ((nodes + 1) >> 1);
+        const int mine = half ? nodes - first : (nodes + 1) >> 1;        // this CTA's nodes: its half of the columns
         for (int c = 0; c < NCH && ok; ++c, ++it) {
           const uint32_t st = it % NQ;
           if (!(ok = pipe.wait_warp(Q_FREE + st, ((it / NQ) & 1u) ^ 1u))) break;
-          const uint32_t bar = pipe.bar(Q_FULL + st), dst = base + OFF_Q + st * QSTAGE;
+          const uint32_t bar = even(Q_FULL + st), dst = base + OFF_Q + st * QSTAGE;
           const CUtensorMap* map = c < 8 ? &tm_qa : &tm_qr;
           const int x = c < 8 ? c * 64 : 0;
-          if (lane == 0) mbar_arrive_expect_tx(bar, (p.linear ? p.linear : nodes * p.H) * 128);
+          if (lane == 0 && half == 0)
+            mbar_arrive_expect_tx(pipe.bar(Q_FULL + st), (p.linear ? 2 * p.linear : nodes * p.H) * 128);
           __syncwarp();
           if (p.linear) {
-            if (lane == 0) tma_load_3d(dst, map, x, ((int64_t)cur.b * p.n + m0) * p.H, 0, bar);
+            if (lane == 0) tma_load_3d_pair(dst, map, x, ((int64_t)cur.b * p.n + m0 + first) * p.H, 0, bar);
           } else {
-            for (int i = lane; i < nodes; i += 32)
-              tma_load_3d(dst + i * p.Hp * 128, map, x, (cur.b * p.n + node_at(p, cur.b, m0 + i)) * p.H, 0, bar);
+            for (int i = lane; i < mine; i += 32)
+              tma_load_3d_pair(dst + i * p.Hp * 128, map, x,
+                               (cur.b * p.n + node_at(p, cur.b, m0 + first + i)) * p.H, 0, bar);
           }
           __syncwarp();
         }
       }
     }
-    for (uint32_t j = it > NQ ? it - NQ : 0; j < it; ++j) pipe.drain(Q_FULL + j % NQ, (j / NQ) & 1u);
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ MMA
+    if (half == 0)
+      for (uint32_t j = it > NQ ? it - NQ : 0; j < it; ++j) pipe.drain(Q_FULL + j % NQ, (j / NQ) & 1u);
+  } else if (warp == 2 && half == 0) {
+    // ------------------------------------------------------------ MMA (one thread of the even CTA)
     uint32_t it = 0, ts = 0, un = 0;
-    bool ok = true;
+    uint32_t ok = 1;
     while (ok && cur.next(p, bad)) {
-      if (bad || rank >= cur.tiles) continue;
-      for (int t = rank; t < cur.tiles && ok; t += csize, ++ts) {
-        const int nodes = min(p.per_tile, cur.count - t * p.per_tile);
-        const uint32_t idesc = idesc_bf16(BK, nodes * p.Hp, 0, 0);
-        const uint32_t sb = ts % NS, d = tmem + sb * BN;
-        const bool first = t == rank, last = t + csize >= cur.tiles;
-        if (!(ok = pipe.wait_warp(S_FREE + sb, ((ts / NS) & 1u) ^ 1u))) break;
-        tc_fence_after();
-        for (int c = 0; c < NCH; ++c, ++it) {
-          const uint32_t st = it % NQ;
-          if (first && !(ok = pipe.wait_warp(K_FULL + c, un & 1u))) break;
-          if (!(ok = pipe.wait_warp(Q_FULL + st, (it / NQ) & 1u))) break;
-          if (lane == 0) {
+      if (bad || pr >= cur.tiles) continue;
+      const int tiles = __shfl_sync(0xffffffffu, cur.tiles, 0), count = __shfl_sync(0xffffffffu, cur.count, 0);
+      if (elect_one()) {
+        uint32_t i = it, s = ts;
+        for (int t = pr; t < tiles && ok; t += pairs, ++s) {
+          const int nodes = min(p.per_tile, count - t * p.per_tile);
+          const uint32_t idesc = idesc_bf16(UK, 2 * ((nodes + 1) >> 1) * p.Hp, 0, 0);
+          const uint32_t sb = s % NS, d = tmem + sb * BN;
+          const bool first = t == pr, last = t + pairs >= tiles;
+          if (!(ok = pipe.wait_remote(S_FREE + sb, ((s / NS) & 1u) ^ 1u))) break;
+          tc_fence_after();
+          for (int c = 0; c < NCH; ++c, ++i) {
+            const uint32_t st = i % NQ;
+            if (first && !(ok = pipe.wait(K_FULL + c, un & 1u))) break;
+            if (!(ok = pipe.wait(Q_FULL + st, (i / NQ) & 1u))) break;
+            tc_fence_after();
             const uint64_t a = desc_of(base + OFF_K + c * KCHUNK), b = desc_of(base + OFF_Q + st * QSTAGE);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16_ss(d, a + 2 * k, b + 2 * k, idesc, c + k > 0);
-            tc_commit(pipe.bar(Q_FREE + st));
-            if (last) tc_commit(pipe.bar(K_FREE + c));
+            for (int k = 0; k < 4; ++k) mma_bf16_ss_pair(d, a + 2 * k, b + 2 * k, idesc, c + k > 0);
+            tc_commit_pair(pipe.bar(Q_FREE + st), both);
+            if (last) tc_commit_pair(pipe.bar(K_FREE + c), both);
           }
-          __syncwarp();
+          if (ok) tc_commit_pair(pipe.bar(S_FULL + sb), both);
         }
-        if (ok && lane == 0) tc_commit(pipe.bar(S_FULL + sb));
-        __syncwarp();
       }
+      ok = __all_sync(0xffffffffu, ok);
+      const int done = (tiles - pr + pairs - 1) / pairs;
+      it += (uint32_t)done * NCH;
+      ts += (uint32_t)done;
       ++un;
     }
-    if (lane == 0) tc_commit(pipe.bar(DRAIN));
+    if (elect_one()) tc_commit_pair(pipe.bar(DRAIN), (uint16_t)(1u << rank));
     __syncwarp();
     pipe.drain(DRAIN, 0);                               // no MMA in flight when TMEM is released
   } else if (warp == 3) {
@@ -310,10 +328,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
     bool ok = true;
     while (ok && cur.next(p, bad)) {
       if (bad) continue;
-      const bool tail = (int64_t)(cur.kt + 1) * BK > cur.L;
-      for (int t = rank; t < cur.tiles; t += csize, ++ts) {
+      const bool tail = (int64_t)cur.kt * UK + half * BK + BK > cur.L;
+      for (int t = pr; t < cur.tiles; t += pairs, ++ts) {
         const uint32_t sb = ts % NS;
-        if (!(ok = pipe.wait_warp(S_FREE + sb, ((ts / NS) & 1u) ^ 1u))) break;
+        if (!(ok = pipe.wait_warp(Z_FREE + sb, ((ts / NS) & 1u) ^ 1u))) break;
         float* z = reinterpret_cast<float*>(gbase + OFF_Z) + sb * BN;
         uint8_t* col = gbase + OFF_NODE + sb * BN;
         uint32_t* vis = reinterpret_cast<uint32_t*>(gbase + OFF_VIS) + sb * 128 * 4;
@@ -337,9 +355,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         mbar_arrive(pipe.bar(Z_FULL + sb));
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int tid = threadIdx.x - 128, g = tid >> 7, r = tid & 127;       // group, key of the unit
+    const int tid = threadIdx.x - 128, g = tid >> 7, r = tid & 127;       // group, key of the CTA
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t ts = 0, un = 0;
     bool ok = true;
@@ -366,15 +384,15 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         }
       out = named_bar_red_or(1, 256, out);
       // a group that gave up at the end of the last unit takes the other one with it
-      if (csize > 1 && named_bar_red_or(1, 256, !ok)) break;
-      const int64_t key = (int64_t)cur.kt * BK + r;
+      if (pairs > 1 && named_bar_red_or(1, 256, !ok)) break;
+      const int64_t key0 = (int64_t)cur.kt * UK + half * BK, key = key0 + r;
       const int k = key < cur.L ? -1 : (int)(key - cur.L);                // node of a tree slot
-      const bool tail = (int64_t)(cur.kt + 1) * BK > cur.L;
+      const bool tail = key0 + BK > cur.L;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int t = rank; t < cur.tiles; t += csize, ++ts) {
+      for (int t = pr; t < cur.tiles; t += pairs, ++ts) {
         const uint32_t sb = ts % NS, par = (ts / NS) & 1u;
         const int rows = min(p.per_tile, cur.count - t * p.per_tile) * p.Hp;
-        ok = pipe.wait(Z_FULL + sb, par) && pipe.wait(S_FULL + sb, par);
+        ok = pipe.wait(Z_FULL + sb, par) && pipe.wait_remote(S_FULL + sb, par);
         if (named_bar_red_or(1, 256, !ok)) {
           ok = false;
           break;
@@ -416,10 +434,14 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
             }
         }
         tc_fence_before();
-        mbar_arrive(pipe.bar(S_FREE + sb));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(pipe.bar(Z_FREE + sb));
+          mbar_arrive_remote(even(S_FREE + sb));
+        }
       }
       if (!ok) break;
-      // the two groups' sums, then the other CTAs' in rank order
+      // the two groups' sums, then the other pairs' in order
       float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       float* x = reinterpret_cast<float*>(gbase + OFF_X) + (un & 1) * BK;
       if (g == 1) x[r] = sum;
@@ -428,16 +450,16 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
       ++un;
       if (g == 0) {
         sum += x[r];
-        if (csize > 1 && rank > 0) {
+        if (pr > 0) {
           if (!(ok = __all_sync(0xffffffffu, pipe.wait_remote(P_FREE + slot, turn ^ 1u)))) continue;
-          const uint32_t to = map_to_rank(base + OFF_PART + ((slot * (MAXC - 1) + rank - 1) * BK + r) * 4, 0);
+          const uint32_t to = map_to_rank(base + OFF_PART + ((slot * (MAXP - 1) + pr - 1) * BK + r) * 4, (uint32_t)half);
           st_cluster_u32(to, __float_as_uint(sum));
-          mbar_arrive_remote(map_to_rank(pipe.bar(P_FULL + slot), 0));
+          mbar_arrive_remote(map_to_rank(pipe.bar(P_FULL + slot), (uint32_t)half));
         } else {
-          if (csize > 1) {
+          if (pairs > 1) {
             if (!(ok = __all_sync(0xffffffffu, pipe.wait_remote(P_FULL + slot, turn)))) continue;
-            const float* part = reinterpret_cast<const float*>(gbase + OFF_PART) + slot * (MAXC - 1) * BK;
-            for (int i = 0; i < csize - 1; ++i) sum += part[i * BK + r];
+            const float* part = reinterpret_cast<const float*>(gbase + OFF_PART) + slot * (MAXP - 1) * BK;
+            for (int i = 0; i < pairs - 1; ++i) sum += part[i * BK + r];
           }
           if (!out) {
             float* wo = p.w_out + (int64_t)cur.b * p.wo;
@@ -449,9 +471,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
                   if (p.path[(size_t)cur.b * p.n + m] == k) wo[cur.L + m] = sum;
             }
           }
-          if (csize > 1) {
+          if (pairs > 1) {
             named_bar_sync(2, 128);                     // everyone has read the parts
-            if (r < csize - 1) mbar_arrive_remote(map_to_rank(pipe.bar(P_FREE + slot), r + 1));
+            if (r < pairs - 1) mbar_arrive_remote(map_to_rank(pipe.bar(P_FREE + slot), (uint32_t)(2 * (r + 1) + half)));
           }
         }
       }
@@ -459,11 +481,13 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
-  if (csize > 1) cluster_sync();                        // no CTA leaves while another writes to it
+  cluster_sync();                       // no CTA leaves, or frees its TMEM, while another works on it
   if (warp == 3) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
+  __syncwarp();
+  cluster_sync();
 }
 
 }  // namespace aw
@@ -471,11 +495,11 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
 
 using namespace kd;
 
-// Clusters of `c` CTAs that fit on the device at once (cached per device).
+// Clusters of `c` CTAs (2, 4 or 8) that fit on the device at once (cached per device).
 static int active_clusters(int c, int sms) {
-  static std::atomic<int> cached[64][4];
+  static std::atomic<int> cached[64][3];
   int dev = 0;
-  const int slot = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3;
+  const int slot = c == 2 ? 0 : c == 4 ? 1 : 2;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms / c;
   int v = cached[dev][slot].load(std::memory_order_relaxed);
   if (v > 0) return v;
@@ -541,10 +565,9 @@ static int weights_impl(const kd_bf16_t* qa, const kd_bf16_t* qr, const kd_bf16_
   p.P = pt ? page : 0;
   p.M = (int)M;
   p.Hp = (H + 15) / 16 * 16;
-  p.per_tile = aw::BN / p.Hp;
+  p.per_tile = aw::BN / p.Hp & ~1;
   const int64_t rows = (int64_t)B * n * H;
-  const int tile_rows = (p.per_tile < n ? p.per_tile : n) * H;
-  p.linear = !path && H % 16 == 0 ? tile_rows : 0;
+  p.linear = !path && H % 16 == 0 ? ((p.per_tile < n ? p.per_tile : n) + 1) / 2 * H : 0;
   p.kbox = pt && page < aw::BK ? page : aw::BK;
   p.scale_log2 = scale * 1.4426950408889634f;
   const uint32_t qbox = (uint32_t)(p.linear ? p.linear : H);
@@ -554,30 +577,30 @@ static int weights_impl(const kd_bf16_t* qa, const kd_bf16_t* qr, const kd_bf16_
   if ((st = make_tmap3(&tc, c, KD_D_C, (uint64_t)cache_rows, 1, sc, 0, (uint32_t)p.kbox, 1))) return st;
   if ((st = make_tmap3(&tr, r, KD_D_R, (uint64_t)cache_rows, 1, sr, 0, (uint32_t)p.kbox, 1))) return st;
 
-  // Cluster size: the one with the shortest longest run of query tiles, were every request
-  // of length cap.  A path is short as a rule (acceptance ends within a few nodes), so it
-  // counts as at most four nodes.
-  const int64_t units = B * ((cap + aw::BK - 1) / aw::BK);
+  // Pairs of a cluster: the number with the shortest longest run of query tiles, were every
+  // request of length cap.  A path is short as a rule (acceptance ends within a few nodes), so
+  // it counts as at most four nodes.
+  const int64_t units = B * ((cap + aw::UK - 1) / aw::UK);
   const int nodes = path && n > 4 ? 4 : n;
   const int64_t qt = (nodes + p.per_tile - 1) / p.per_tile;
   int best = 1, fit = 0;
   double cost = 1e300;
-  for (int cs = 1; cs <= aw::MAXC; cs *= 2) {
-    if (cs > 1 && cs > qt) break;
-    const int nc = active_clusters(cs, sms);
-    const double t = (double)((units + nc - 1) / nc) * ((double)((qt + cs - 1) / cs) + 0.3);
-    if (t < 0.95 * cost) cost = t, best = cs, fit = nc;
+  for (int c = 1; c <= aw::MAXP; c *= 2) {
+    if (c > 1 && c > qt) break;
+    const int nc = active_clusters(2 * c, sms);
+    const double t = (double)((units + nc - 1) / nc) * ((double)((qt + c - 1) / c) + 0.3);
+    if (t < 0.95 * cost) cost = t, best = c, fit = nc;
   }
   if (units > INT32_MAX) return KD_EINVAL;
   const int64_t clusters = units < fit ? units : fit;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * best));
+  cfg.gridDim = dim3((unsigned)(clusters * 2 * best));
   cfg.blockDim = dim3(aw::THREADS);
   cfg.dynamicSmemBytes = aw::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)best;
+  at.val.clusterDim.x = (unsigned)(2 * best);
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
