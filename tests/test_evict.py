@@ -224,6 +224,28 @@ def test_weights_of_true_lse_sum_to_one(kd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,hi,n,H", [(64, 3000, 17, 64), (150, 700, 3, 16), (16, 4000, 1, 64), (40, 900, 40, 5)])
+def test_weights_launch_after_launch(kd, B, hi, n, H):
+    """Many units per CTA with one to many query tiles in turn, a hundred launches behind each
+    other: no wait gives up and the bits stay the same."""
+    rng = np.random.RandomState(B)
+    trees = [tree(n, 3 * b + 1) for b in range(B)]
+    vis = torch.from_numpy(np.stack([t[1] for t in trees]).view(np.int32)).cuda()
+    paths = [t[2] if b % 3 else [0] for b, t in enumerate(trees)]
+    path, alen = i32([p + [-1] * (n - len(p)) for p in paths]), i32([len(p) for p in paths])
+    lens = i32(rng.randint(1, hi, B).tolist())
+    cap = hi + n
+    qa, qr = normal(B, n, H, 512, seed=1, scale=0.5), normal(B, n, H, 64, seed=2, scale=0.5)
+    c, r = normal(B, cap, 512, seed=3), normal(B, cap, 64, seed=4)
+    lse, err = torch.full((B, n, H), 8.0, device="cuda"), kd.new_error_word()
+    w = [torch.zeros(B, cap, device="cuda") for _ in range(2)]
+    for i in range(100):
+        kd.kd_kv_attn_weights(qa, qr, c, r, lens, vis, lse, path=path, length=alen, weights_out=w[i > 0], dev_error=err)
+    assert kd.kd_read_device_error(err) == 0
+    assert torch.equal(*w)
+
+
+@pytest.mark.gpu
 def test_weights_device_errors(kd):
     B, n, H, cap = 6, 4, 2, 64
     qa, qr = normal(B, n, H, 512, seed=1), normal(B, n, H, 64, seed=2)

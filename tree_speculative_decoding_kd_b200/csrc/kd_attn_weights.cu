@@ -7,23 +7,25 @@
 // and adds up along its own columns: no reduction between threads, no second product, a
 // fixed order.  With the rows' lse known, one pass is enough: nothing runs a maximum.
 //
-// Two CTAs work as a pair (cta_group::2): M = 256 keys, 128 in each CTA's shared memory
-// (nine 16 KB chunks of 64 columns, there for the unit), while each CTA holds only half of
-// the query rows of a chunk.  The query rows stream past the keys from L2 at 32 bytes a
-// cycle and SM, half of what one CTA alone would need for the tensor pipe's rate, and the
-// 64 KB that are left for them hold four stages instead of two.  (Alone, a CTA with two
-// 32 KB stages waited for L2: 588 us for 4 x 16384 keys and 8192 rows, 195 us for the
-// accepted paths of 64 requests.)  A K chunk is refilled for the next unit as soon as the
-// last query tile has used it, so that with few rows (one query tile: bound by the cache's
-// bytes) the next unit's keys stream in behind the current one's products.
+// Two CTAs work as a pair (cta_group::2): M = 256 keys, 128 in each CTA's shared memory,
+// while each CTA holds only half of the query rows.  The query rows then stream from L2 at
+// 32 bytes a cycle and SM, half of what one CTA alone would need for the tensor pipe's rate.
+// Shared memory is thirteen 16 KB stages of 64 columns: the unit's keys stay in nine of them,
+// the query rows pass through four.  A chunk of keys is refilled for the next unit as soon as
+// the last query tile has used it, so that with few rows (one query tile, as for an accepted
+// path: bound by the cache's bytes) the next unit's keys stream in behind this one's products.
+// Measured (one B200): 4 x 16384 keys against 8192 rows 500 us (1.25 PFLOP/s at the power
+// cap, 1.4 cold); the accepted paths of 64 requests 165 to 185 us (3.7 to 4.1 TB/s of keys).
+// One CTA alone, with two 32 KB stages for the query rows, took 588 and 195 us.  Letting the
+// keys pass through 6, 8, 10 or 11 of the stages instead of keeping them cost 3 to 20% for the
+// accepted paths: fewer bytes of keys on their way, or too few query stages.
 //
 // A unit is (request, 256 keys); a cluster of 1, 2 or 4 pairs shares a unit by dealing the
 // query tiles out among its pairs, whose sums meet in the first pair's shared memory.
 //
 // Query tiles hold whole nodes: rows of one node are contiguous in memory, nodes on an
-// accepted path are not, so a stage is filled by one box per node, 16-row aligned (rows
-// that pad a node up are zeroed once and get lse = inf).  When every node counts and H is a
-// multiple of 16, one box fills the stage.
+// accepted path are not, so a stage is filled by one box per node, 16-row aligned.  When every
+// node counts and H is a multiple of 16, one box fills the stage.
 //
 // Roles in each CTA: warp 0 loads K, warp 1 loads Q, warp 2 (one thread, even CTA) issues the
 // MMAs, warp 3 stages the rows' lse and masks, warps 4 to 11 are the epilogue (two groups of
@@ -48,15 +50,14 @@ constexpr int BK = 128;                       // keys per CTA
 constexpr int UK = 2 * BK;                    // keys per unit
 constexpr int BN = 256;                       // query rows per tile
 constexpr int NCH = 9;                        // 64-column chunks: 8 latent, 1 rope
-constexpr int KCHUNK = BK * 128;              // bytes
-constexpr int QSTAGE = BN / 2 * 128;          // a CTA's half of the rows
-constexpr int NQ = 4;                         // Q ring stages
+constexpr int STAGE = BK * 128;               // bytes: 128 keys, or a CTA's half of the query rows
+constexpr int NQ = 4;                         // stages of the query rows
 constexpr int NS = 2;                         // S tiles in TMEM
 constexpr int MAXP = 4;                       // pairs of a cluster
 
 enum Bar {
   K_FULL = 0,                   // even CTA: both CTAs' chunk landed (TMA)
-  K_FREE = K_FULL + NCH,        // chunk used for the last time in its unit (MMA commit, both CTAs)
+  K_FREE = K_FULL + NCH,        // chunk used for the last time (MMA commit, both CTAs)
   Q_FULL = K_FREE + NCH,        // even CTA: both halves landed
   Q_FREE = Q_FULL + NQ,         // stage used (both CTAs)
   Z_FULL = Q_FREE + NQ,         // lse and masks of the tile staged (32 arrivals)
@@ -70,13 +71,12 @@ enum Bar {
 };
 constexpr int OFF_ABORT = 512, OFF_TMEM = 516;
 constexpr int OFF_Z = 1024;                             // f32 [NS][256]: -lse log2(e), -inf for a row that adds nothing
-constexpr int OFF_NODE = OFF_Z + NS * BN * 4;           // u8 [NS][256]: node of each column
-constexpr int OFF_VIS = OFF_NODE + NS * BN;             // u32 [NS][128][4]: masks of the tile's nodes, by place in the tile
+constexpr int OFF_NODE = OFF_Z + NS * BN * 4;           // u8 [NS][16]: node of each 16 columns
+constexpr int OFF_VIS = OFF_NODE + 64;                 // u32 [NS][128][4]: masks of the tile's nodes, by place in the tile
 constexpr int OFF_X = OFF_VIS + NS * 128 * 16;          // f32 [2][128]: sums of the second group
 constexpr int OFF_PART = OFF_X + 2 * BK * 4;            // f32 [2][MAXP - 1][128]: sums of the other pairs
-constexpr int OFF_K = ((OFF_PART + 2 * (MAXP - 1) * BK * 4 + 1023) / 1024) * 1024;
-constexpr int OFF_Q = OFF_K + NCH * KCHUNK;
-constexpr int SMEM = OFF_Q + NQ * QSTAGE + 1024;
+constexpr int OFF_STAGE = ((OFF_PART + 2 * (MAXP - 1) * BK * 4 + 1023) / 1024) * 1024;
+constexpr int SMEM = OFF_STAGE + (NCH + NQ) * STAGE + 1024;
 static_assert(NBAR * 8 <= OFF_ABORT && SMEM <= 232448, "shared memory");
 
 struct Params {
@@ -100,17 +100,17 @@ struct Cursor {
   int64_t L;
   int count, tiles;             // counted nodes, query tiles
   int base, b0, incl, step, u;  // window of 32 requests: first request, units before it, inclusive sums
-  __device__ __forceinline__ static int units_of(const Params& p, int b) {
-    if (b >= p.B) return 0;
-    const int64_t L = p.lens[b];
-    if (L < 0 || L + p.n > p.cap) return 1;             // one unit that reports it
-    const int c = p.path ? p.len[b] : p.n;
-    if (c < 1 || c > p.n) return 1;
-    return (int)((L + p.n + UK - 1) / UK);
+  int len_l, count_l;           // lane i: committed length and counted nodes of request b0 + i
+  __device__ __forceinline__ static int bad_of(const Params& p, int64_t L, int count) {
+    return L < 0 || L + p.n > p.cap ? KD_DEV_CACHE_FULL : count < 1 || count > p.n ? KD_DEV_BAD_PATH : 0;
   }
   __device__ __forceinline__ void window(const Params& p, int first) {
     b0 = first;
-    incl = units_of(p, b0 + (threadIdx.x & 31));
+    const int i = b0 + (threadIdx.x & 31);
+    len_l = i < p.B ? p.lens[i] : 0;
+    count_l = i < p.B && p.path ? p.len[i] : p.n;
+    // a request without work has one unit, which reports it
+    incl = i >= p.B ? 0 : bad_of(p, len_l, count_l) ? 1 : (int)(((int64_t)len_l + p.n + UK - 1) / UK);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -134,16 +134,14 @@ struct Cursor {
       total = __shfl_sync(0xffffffffu, incl, 31);
     }
     const int at = u - base;
-    const unsigned past = __ballot_sync(0xffffffffu, incl <= at);
-    const int i = __popc(past);
+    const int i = __popc(__ballot_sync(0xffffffffu, incl <= at));
     b = b0 + i;
     const int before = __shfl_sync(0xffffffffu, incl, i ? i - 1 : 0);
     kt = at - (i ? before : 0);
-    L = p.lens[b];
-    bad = 0;
-    count = p.path ? p.len[b] : p.n;
-    if (L < 0 || L + p.n > p.cap) bad = KD_DEV_CACHE_FULL;
-    else if (count < 1 || count > p.n) bad = KD_DEV_BAD_PATH;
+    b = __shfl_sync(0xffffffffu, b, 0);                 // (uniform to the compiler too)
+    L = __shfl_sync(0xffffffffu, len_l, i);
+    count = __shfl_sync(0xffffffffu, count_l, i);
+    bad = bad_of(p, L, count);
     tiles = bad ? 0 : (count + p.per_tile - 1) / p.per_tile;
     return true;
   }
@@ -177,14 +175,12 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank(), half = rank & 1, pr = rank >> 1;
   const int cluster = blockIdx.x / (2 * pairs), clusters = gridDim.x / (2 * pairs);
+  const uint32_t k_at = base + OFF_STAGE, q_at = k_at + NCH * STAGE;
   const uint16_t both = (uint16_t)(3u << (rank & ~1));
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
   const Pipe pipe{base, abort_flag, p.err};
   auto even = [&](int bar) { return map_to_rank(pipe.bar(bar), (uint32_t)(rank & ~1)); };
 
-  // the rows that pad a node stay zero: no box ever writes them
-  for (int i = threadIdx.x; i < NQ * QSTAGE / 16; i += THREADS)
-    reinterpret_cast<uint4*>(gbase + OFF_Q)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     for (int i = 0; i < NBAR; ++i) {
@@ -194,7 +190,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
     }
     fence_mbar_init();
   }
-  fence_proxy_async_cta();
   if (warp == 3) {
     tmem_alloc_pair(base + OFF_TMEM, 512);
     tmem_relinquish_pair();
@@ -238,9 +233,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         if (!(ok = pipe.wait_warp(K_FREE + c, (it & 1u) ^ 1u))) break;
         if (lane == 0) {
           const uint32_t bar = even(K_FULL + c);
-          if (half == 0) mbar_arrive_expect_tx(pipe.bar(K_FULL + c), 2 * KCHUNK);
+          if (half == 0) mbar_arrive_expect_tx(pipe.bar(K_FULL + c), 2 * STAGE);
           for (int i = 0; i < boxes; ++i)
-            tma_load_3d_pair(base + OFF_K + c * KCHUNK + i * p.kbox * 128, c < 8 ? &tm_c : &tm_r, c < 8 ? c * 64 : 0,
+            tma_load_3d_pair(k_at + c * STAGE + i * p.kbox * 128, c < 8 ? &tm_c : &tm_r, c < 8 ? c * 64 : 0,
                              (int32_t)row[i], 0, bar);
         }
         __syncwarp();
@@ -260,23 +255,24 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
       if (bad) continue;
       for (int t = pr; t < cur.tiles && ok; t += pairs) {
         const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0), first = half * ((nodes + 1) >> 1);
-        const int mine = half ? nodes - first : (nodes + 1) >> 1;        // this CTA's nodes: its half of the columns
-        for (int c = 0; c < NCH && ok; ++c, ++it) {
+        // This CTA's nodes: its half of the columns.  The odd CTA always has one, the last one
+        // again where there is none for it: were a stage filled without it, the even CTA could
+        // go round the stage's barriers once more before the odd one looked at them.
+        const int mine = half ? max(1, nodes >> 1) : (nodes + 1) >> 1, boxes = ((nodes + 1) >> 1) + max(1, nodes >> 1);
+        const int bytes = (p.linear ? 2 * p.linear : boxes * p.H) * 128;
+        // lane i has the box of this CTA's node i (8 at most): first row of the flat [B n H] query
+        const int row = p.linear ? (cur.b * p.n + m0 + first) * p.H
+                                 : (cur.b * p.n + node_at(p, cur.b, m0 + min(first + lane, nodes - 1))) * p.H;
+        const bool issue = p.linear ? lane == 0 : lane < mine;
+        for (int c = 0; c < NCH; ++c, ++it) {
           const uint32_t st = it % NQ;
           if (!(ok = pipe.wait_warp(Q_FREE + st, ((it / NQ) & 1u) ^ 1u))) break;
-          const uint32_t bar = even(Q_FULL + st), dst = base + OFF_Q + st * QSTAGE;
-          const CUtensorMap* map = c < 8 ? &tm_qa : &tm_qr;
-          const int x = c < 8 ? c * 64 : 0;
-          if (lane == 0 && half == 0)
-            mbar_arrive_expect_tx(pipe.bar(Q_FULL + st), (p.linear ? 2 * p.linear : nodes * p.H) * 128);
+          const uint32_t bar = even(Q_FULL + st);
+          if (lane == 0 && half == 0) mbar_arrive_expect_tx(pipe.bar(Q_FULL + st), bytes);
           __syncwarp();
-          if (p.linear) {
-            if (lane == 0) tma_load_3d_pair(dst, map, x, ((int64_t)cur.b * p.n + m0 + first) * p.H, 0, bar);
-          } else {
-            for (int i = lane; i < mine; i += 32)
-              tma_load_3d_pair(dst + i * p.Hp * 128, map, x,
-                               (cur.b * p.n + node_at(p, cur.b, m0 + first + i)) * p.H, 0, bar);
-          }
+          if (issue)
+            tma_load_3d_pair(q_at + st * STAGE + lane * p.Hp * 128, c < 8 ? &tm_qa : &tm_qr, c < 8 ? c * 64 : 0, row, 0,
+                             bar);
           __syncwarp();
         }
       }
@@ -285,39 +281,36 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
       for (uint32_t j = it > NQ ? it - NQ : 0; j < it; ++j) pipe.drain(Q_FULL + j % NQ, (j / NQ) & 1u);
   } else if (warp == 2 && half == 0) {
     // ------------------------------------------------------------ MMA (one thread of the even CTA)
-    uint32_t it = 0, ts = 0, un = 0;
-    uint32_t ok = 1;
+    uint32_t un = 0, qc = 0, ts = 0, ok = 1;            // units, chunks of query rows, tiles
     while (ok && cur.next(p, bad)) {
       if (bad || pr >= cur.tiles) continue;
-      const int tiles = __shfl_sync(0xffffffffu, cur.tiles, 0), count = __shfl_sync(0xffffffffu, cur.count, 0);
+      const int todo = (cur.tiles - pr + pairs - 1) / pairs;
       if (elect_one()) {
-        uint32_t i = it, s = ts;
-        for (int t = pr; t < tiles && ok; t += pairs, ++s) {
-          const int nodes = min(p.per_tile, count - t * p.per_tile);
+        uint32_t q = qc, s = ts;
+        for (int t = 0; t < todo && ok; ++t, ++s) {
+          const int nodes = min(p.per_tile, cur.count - (pr + t * pairs) * p.per_tile);
           const uint32_t idesc = idesc_bf16(UK, 2 * ((nodes + 1) >> 1) * p.Hp, 0, 0);
           const uint32_t sb = s % NS, d = tmem + sb * BN;
-          const bool first = t == pr, last = t + pairs >= tiles;
           if (!(ok = pipe.wait_remote(S_FREE + sb, ((s / NS) & 1u) ^ 1u))) break;
           tc_fence_after();
-          for (int c = 0; c < NCH; ++c, ++i) {
-            const uint32_t st = i % NQ;
-            if (first && !(ok = pipe.wait(K_FULL + c, un & 1u))) break;
-            if (!(ok = pipe.wait(Q_FULL + st, (i / NQ) & 1u))) break;
+          for (int c = 0; c < NCH; ++c, ++q) {
+            const uint32_t st = q % NQ;
+            if (t == 0 && !(ok = pipe.wait(K_FULL + c, un & 1u))) break;
+            if (!(ok = pipe.wait(Q_FULL + st, (q / NQ) & 1u))) break;
             tc_fence_after();
-            const uint64_t a = desc_of(base + OFF_K + c * KCHUNK), b = desc_of(base + OFF_Q + st * QSTAGE);
+            const uint64_t a = desc_of(k_at + c * STAGE), b = desc_of(q_at + st * STAGE);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16_ss_pair(d, a + 2 * k, b + 2 * k, idesc, c + k > 0);
+            for (int i = 0; i < 4; ++i) mma_bf16_ss_pair(d, a + 2 * i, b + 2 * i, idesc, c + i > 0);
             tc_commit_pair(pipe.bar(Q_FREE + st), both);
-            if (last) tc_commit_pair(pipe.bar(K_FREE + c), both);
+            if (t + 1 == todo) tc_commit_pair(pipe.bar(K_FREE + c), both);
           }
           if (ok) tc_commit_pair(pipe.bar(S_FULL + sb), both);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      const int done = (tiles - pr + pairs - 1) / pairs;
-      it += (uint32_t)done * NCH;
-      ts += (uint32_t)done;
       ++un;
+      qc += todo * NCH;
+      ts += todo;
     }
     if (elect_one()) tc_commit_pair(pipe.bar(DRAIN), (uint16_t)(1u << rank));
     __syncwarp();
@@ -333,7 +326,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         const uint32_t sb = ts % NS;
         if (!(ok = pipe.wait_warp(Z_FREE + sb, ((ts / NS) & 1u) ^ 1u))) break;
         float* z = reinterpret_cast<float*>(gbase + OFF_Z) + sb * BN;
-        uint8_t* col = gbase + OFF_NODE + sb * BN;
+        uint8_t* node16 = gbase + OFF_NODE + sb * (BN / 16);
         uint32_t* vis = reinterpret_cast<uint32_t*>(gbase + OFF_VIS) + sb * 128 * 4;
         const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0);
 #pragma unroll
@@ -345,7 +338,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
             v = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
           }
           z[j] = v;
-          if (tail) col[j] = (uint8_t)(i < nodes ? i : 0);
+          if (tail && (j & 15) == 0) node16[j >> 4] = (uint8_t)(i < nodes ? i : 0);
         }
         if (tail)
           for (int i = lane; i < nodes; i += 32) {
@@ -367,27 +360,21 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         if (tid == 0 && rank == 0) raise_dev_error(p.err, bad);
         continue;
       }
-      // every CTA's view of the request: the same answer in all of them
-      bool out = false;
-      if (p.path && r < cur.count) {
-        const int k = p.path[(size_t)cur.b * p.n + r];
-        out = k < 0 || k >= p.n;
-        if (out) raise_dev_error(p.err, KD_DEV_BAD_PATH);
-      }
-      if (p.P)
-        for (int64_t q = tid; q * p.P < cur.L + p.n; q += 256) {
-          const int32_t id = p.pt[(size_t)cur.b * p.M + q];
-          if (id < 0 || id >= p.pages) {
-            out = true;
-            raise_dev_error(p.err, KD_DEV_BAD_PAGE);
-          }
-        }
-      out = named_bar_red_or(1, 256, out);
       // a group that gave up at the end of the last unit takes the other one with it
       if (pairs > 1 && named_bar_red_or(1, 256, !ok)) break;
       const int64_t key0 = (int64_t)cur.kt * UK + half * BK, key = key0 + r;
       const int k = key < cur.L ? -1 : (int)(key - cur.L);                // node of a tree slot
       const bool tail = key0 + BK > cur.L;
+      // asked for before the scores are ready, looked at when they are summed up: what was
+      // there, and every CTA's own look at the request's path and pages
+      const float was = k < 0 && p.w_in && g == 0 ? p.w_in[(int64_t)cur.b * p.wi + key] : 0.f;
+      const int node = p.path && r < cur.count ? p.path[(size_t)cur.b * p.n + r] : 0;
+      bool bad_page = false;
+      if (p.P)
+        for (int64_t q = tid; q * p.P < cur.L + p.n; q += 256) {
+          const int32_t id = p.pt[(size_t)cur.b * p.M + q];
+          bad_page |= id < 0 || id >= p.pages;
+        }
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       for (int t = pr; t < cur.tiles; t += pairs, ++ts) {
         const uint32_t sb = ts % NS, par = (ts / NS) & 1u;
@@ -400,7 +387,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         tc_fence_after();
         const float* z = reinterpret_cast<const float*>(gbase + OFF_Z) + sb * BN;
         const uint32_t src = tmem + lanes + sb * BN;
-        if (!tail) {
+        if (!tail && p.Hp == p.H) {
           int j = g * 32;
           for (; j + 32 <= rows; j += 64) {
             uint32_t s[32];
@@ -417,20 +404,26 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
             for (int i = 0; i < 16; i += 4) add4(acc, s + i, *reinterpret_cast<const float4*>(z + j + i), p.scale_log2);
           }
         } else {
-          const uint8_t* col = gbase + OFF_NODE + sb * BN;
+          // sixteen columns are of one node: seen or not together
+          const uint8_t* node16 = gbase + OFF_NODE + sb * (BN / 16);
           const uint32_t* vis = reinterpret_cast<const uint32_t*>(gbase + OFF_VIS) + sb * 128 * 4;
           for (int j = g * 32; j < rows; j += 64)
-            for (int q = 0; q < 32 && j + q < rows; q += 16) {
+            for (int q = j; q < j + 32 && q < rows; q += 16) {
               uint32_t s[16];
-              tmem_ld16(src + j + q, s);
+              tmem_ld16(src + q, s);
+              const bool see = k < 0 || (k < p.n && (vis[node16[q >> 4] * 4 + (k >> 5)] >> (k & 31) & 1u));
               tmem_wait_ld();
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              if (p.Hp == p.H) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int jj = j + q + i;
-                const bool see = k < 0 || (k < p.n && (vis[col[jj] * 4 + (k >> 5)] >> (k & 31) & 1u));
-                const float e = ex2(__uint_as_float(s[i]) * p.scale_log2 + z[jj]);
-                acc[i & 3] += see ? e : 0.f;
+                for (int i = 0; i < 16; i += 4) add4(part, s + i, *reinterpret_cast<const float4*>(z + q + i), p.scale_log2);
+              } else {                                  // rows that pad a node hold whatever was there before
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  part[i & 3] += z[q + i] != -INFINITY ? ex2(__uint_as_float(s[i]) * p.scale_log2 + z[q + i]) : 0.f;
               }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[i] += see ? part[i] : 0.f;
             }
         }
         tc_fence_before();
@@ -445,7 +438,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
       float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       float* x = reinterpret_cast<float*>(gbase + OFF_X) + (un & 1) * BK;
       if (g == 1) x[r] = sum;
-      named_bar_sync(1, 256);
+      const bool bad_node = node < 0 || node >= p.n;
+      if (bad_node) raise_dev_error(p.err, KD_DEV_BAD_PATH);
+      if (bad_page) raise_dev_error(p.err, KD_DEV_BAD_PAGE);
+      const bool out = named_bar_red_or(1, 256, bad_node || bad_page);
       const uint32_t slot = un & 1, turn = (un >> 1) & 1u;
       ++un;
       if (g == 0) {
@@ -463,7 +459,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
           }
           if (!out) {
             float* wo = p.w_out + (int64_t)cur.b * p.wo;
-            if (k < 0) wo[key] = sum + (p.w_in ? p.w_in[(int64_t)cur.b * p.wi + key] : 0.f);
+            if (k < 0) wo[key] = sum + was;
             else if (k < p.n) {
               if (!p.path) wo[key] = sum;
               else
