@@ -426,6 +426,39 @@ def _heads(t, name, tokens=None, heads=None, width=None):
     return T, H, D, st, sh
 
 
+def _cache(c, r):
+    """Requests, row strides and capacity of a contiguous cache [B][cap][512] / [B][cap][64]."""
+    if c.dtype is not torch.bfloat16 or r.dtype is not torch.bfloat16:
+        raise ValueError("caches must be bf16")
+    B, cap, dc = c.shape
+    if dc != D_C or r.shape != (B, cap, D_R):
+        raise ValueError("c_kv must be [B][cap][512] and k_rope [B][cap][64]")
+    cb, sc, c1 = c.stride()
+    rb, sr, r1 = r.stride()
+    if c1 != 1 or r1 != 1 or cb != cap * sc or rb != cap * sr:
+        raise ValueError("cache rows must be unit-stride with uniform row pitch")
+    return B, sc, sr, cap
+
+
+def _pages(c, r, page_table, page_size, B):
+    """Row strides, pages per request and pool size of a paged cache of B requests."""
+    if c.dtype is not torch.bfloat16 or r.dtype is not torch.bfloat16:
+        raise ValueError("page pools must be bf16")
+    rows, dc = c.shape
+    if dc != D_C or r.shape != (rows, D_R):
+        raise ValueError("c_pages must be [rows][512] and r_pages [rows][64]")
+    if page_size < 1 or rows % page_size:
+        raise ValueError("pool rows must be a multiple of page_size")
+    sc, c1 = c.stride()
+    sr, r1 = r.stride()
+    if c1 != 1 or r1 != 1:
+        raise ValueError("pool rows must be unit-stride")
+    _typed(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pages per request]")
+    return sc, sr, page_table.shape[1], rows // page_size
+
+
 def _rope_table(table, rot):
     _typed(table, torch.float32, "rope_table")
     if table.dim() != 2 or (rot is not None and table.shape[1] != rot):
@@ -501,10 +534,10 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
     cu_seqlens None: T / B tokens per request.  Returns q_rope_out (None without queries)."""
     dev = _on_device(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in, q_rope_out,
                dev_error)
-    sc, sr, cap = _cache_strides(c_kv, k_rope)
+    rows, sc, sr, cap = _cache(c_kv, k_rope)
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
                                                        q_rope_in, q_rope_out)
-    if c_kv.shape[0] != B:
+    if rows != B:
         raise ValueError("the cache must hold B requests")
     _check(lib.kd_kv_norm_rope_write(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(kv), kv.stride(0),
                                      _ptr(kv_weight), eps, _ptr(rope_table), max_pos, _ptr(positions),
@@ -519,11 +552,9 @@ def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_l
     """kd_kv_norm_rope_write through a page table."""
     dev = _on_device(c_pages, r_pages, page_table, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in,
                q_rope_out, dev_error)
-    sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
                                                        q_rope_in, q_rope_out)
-    if page_table.shape[0] != B:
-        raise ValueError("page_table must be [B][pages per request]")
+    sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, B)
     _check(lib.kd_kv_norm_rope_write_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
                                            _ptr(cache_lens), _ptr(kv), kv.stride(0), _ptr(kv_weight), eps,
                                            _ptr(rope_table), max_pos, _ptr(positions), interleaved,
@@ -574,7 +605,7 @@ def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu
 
 
 def _weight_rows(w, B, cap, name):
-    if w.dtype != torch.float32 or w.dim() != 2 or w.shape[0] != B or w.shape[1] < cap or w.stride(1) != 1:
+    if w.dtype is not torch.float32 or w.dim() != 2 or w.shape[0] != B or w.shape[1] < cap or w.stride(1) != 1:
         raise ValueError(f"{name} must be fp32 [{B}][at least {cap}] with unit-stride rows")
     return w.stride(0) if B > 1 else max(w.stride(0), w.shape[1])
 
@@ -586,9 +617,9 @@ def _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
     B, n, H, _ = q_abs.shape
     _typed(q_rope, torch.bfloat16, "q_rope", (B, n, H, D_R))
     _typed(cache_lens, torch.int32, "cache_lens", (B,))
-    _need(vis, (torch.int32, torch.uint32), "vis")
-    if tuple(vis.shape) != (B, n, (n + 31) // 32):
-        raise ValueError("vis must be [B][n][ceil(n / 32)]")
+    if (vis.dtype is not torch.int32 and vis.dtype is not torch.uint32) or not vis.is_contiguous() or \
+            vis.shape != (B, n, (n + 31) // 32):
+        raise ValueError("vis must be contiguous int32 or uint32 [B][n][ceil(n / 32)]")
     _typed(lse, torch.float32, "lse", (B, n, H))
     if (path is None) != (length is None):
         raise ValueError("path and length go together")
@@ -608,10 +639,10 @@ def kd_kv_attn_weights(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path=N
     lse is kd_tree_verify_attn's.  Call it before kd_kv_compact: the new slots' weights are
     stored in compacted order.  Returns weights_out (weights_out=weights_in accumulates)."""
     dev = _on_device(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, dev_error)
-    sc, sr, cap = _cache_strides(c_kv, k_rope)
+    rows, sc, sr, cap = _cache(c_kv, k_rope)
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
                                                  weights_out, cap)
-    if c_kv.shape[0] != B:
+    if rows != B:
         raise ValueError("the cache must hold B requests")
     _check(lib.kd_kv_attn_weights(_ptr(q_abs), _ptr(q_rope), _ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens),
                                   _ptr(vis), _ptr(lse), _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
@@ -625,11 +656,9 @@ def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_s
     """kd_kv_attn_weights over a paged cache (page_size 64, 128 or 256)."""
     dev = _on_device(q_abs, q_rope, c_pages, r_pages, page_table, cache_lens, vis, lse, path, length, weights_in,
                weights_out, dev_error)
-    sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
+    sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, cache_lens.shape[0])
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
                                                  weights_out, M * page_size)
-    if page_table.shape[0] != B:
-        raise ValueError("page_table must be [B][pages per request]")
     _check(lib.kd_kv_attn_weights_paged(_ptr(q_abs), _ptr(q_rope), _ptr(c_pages), _ptr(r_pages), sc, sr,
                                         int(page_size), _ptr(page_table), M, N, _ptr(cache_lens), _ptr(vis), _ptr(lse),
                                         _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
@@ -662,16 +691,16 @@ def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_
     cache_lens and weights_in are updated); with them the kept rows go to another cache.
     Returns (kept [B][keep] int32, weights_out, lens_out)."""
     dev = _on_device(c_kv, k_rope, cache_lens, weights_in, c_dst, r_dst, weights_out, lens_out, kept, dev_error)
-    sc, sr, cap = _cache_strides(c_kv, k_rope)
+    rows, sc, sr, cap = _cache(c_kv, k_rope)
     if (c_dst is None) != (r_dst is None):
         raise ValueError("c_dst and r_dst go together")
     inplace = c_dst is None
     if inplace:
         c_dst, r_dst = c_kv, k_rope
-    dc, dr, dcap = _cache_strides(c_dst, r_dst)
+    drows, dc, dr, dcap = _cache(c_dst, r_dst)
     B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, cap, dcap, keep, inplace, weights_out,
                                                          lens_out, kept)
-    if c_kv.shape[0] != B or c_dst.shape[0] != B:
+    if rows != B or drows != B:
         raise ValueError("the caches must hold B requests")
     _check(lib.kd_kv_evict(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(weights_in), wi, int(keep),
                            int(sink), int(recent), B, _ptr(c_dst), _ptr(r_dst), dc, dr, dcap, _ptr(weights_out), wo,
@@ -687,7 +716,7 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
     same pool), which must be none of the source's."""
     dev = _on_device(c_pages, r_pages, page_table, cache_lens, weights_in, c_dst, r_dst, dst_page_table, weights_out,
                lens_out, kept, dev_error)
-    sc, sr, M, N = _page_args(c_pages, r_pages, page_table, page_size)
+    sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, cache_lens.shape[0])
     if (c_dst is None) != (r_dst is None) or (c_dst is not None and dst_page_table is None):
         raise ValueError("c_dst, r_dst and dst_page_table go together")
     inplace = dst_page_table is None
@@ -695,11 +724,9 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
         dst_page_table = page_table
     if c_dst is None:
         c_dst, r_dst = c_pages, r_pages
-    dc, dr, DM, DN = _page_args(c_dst, r_dst, dst_page_table, page_size)
+    dc, dr, DM, DN = _pages(c_dst, r_dst, dst_page_table, page_size, cache_lens.shape[0])
     B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, M * page_size, DM * page_size, keep,
                                                          inplace, weights_out, lens_out, kept)
-    if page_table.shape[0] != B or dst_page_table.shape[0] != B:
-        raise ValueError("page tables must be [B][pages per request]")
     _check(lib.kd_kv_evict_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
                                  _ptr(cache_lens), _ptr(weights_in), wi, int(keep), int(sink), int(recent), B,
                                  _ptr(c_dst), _ptr(r_dst), dc, dr, _ptr(dst_page_table), DM, DN, _ptr(weights_out), wo,
