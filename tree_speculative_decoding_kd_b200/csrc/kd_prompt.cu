@@ -53,7 +53,7 @@ enum Bar {
   V_FULL = K_FREE + NO,             // [NO] its values
   V_FREE = V_FULL + NO,             // [NO]
   V_CLEAN = V_FREE + NO,            // the rows past a sequence's last key are cleared
-  V_GO = V_CLEAN + 1,               // the tile before it is in work
+  V_GO = V_CLEAN + 1,               // that tile is the next its barrier will announce
   Q_FULL = V_GO + 1,                // [2]
   Q_FREE = Q_FULL + 2,              // [2] the unit's last QK MMA of the tile is done
   S_FULL = Q_FREE + 2,              // [2]
@@ -412,6 +412,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (q0 < 0) break;
         const int all = max(n0, n1);
         if (all == 0) continue;
+        // the last value tile may be cleared once the one NO before it, whose barrier it has, is used
+        if (all <= NO && nk < all * BN) mbar_arrive(pipe.bar(V_GO));
         if (!(ok = pipe.wait(K_FULL + kt % NO, (kt / NO) & 1u))) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -428,7 +430,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int j = 0; j < all; ++j, ++kt) {
           const uint32_t v_at = wrap<RING>(pos + KC), next = wrap<RING>(v_at + 2), o = kt % NO, o1 = (kt + 1) % NO;
           const int keys = nk - j * BN;
-          if (j == max(all - 2, 0) && nk < all * BN) mbar_arrive(pipe.bar(V_GO));
+          if (j > 0 && j == all - NO && nk < all * BN) mbar_arrive(pipe.bar(V_GO));
           if (!(ok = pipe.wait(V_FULL + o, (kt / NO) & 1u))) break;
           if (keys < BN) {                                // its tail is being cleared
             if (!(ok = pipe.wait(V_CLEAN, nc & 1u))) break;
