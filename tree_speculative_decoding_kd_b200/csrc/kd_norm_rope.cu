@@ -7,14 +7,18 @@
 // Both are bound by memory (about 7 operations per 4 bytes moved), so every element is
 // read once and written once, 16 bytes at a time.  A lane holds two pieces of eight
 // neighbouring elements of a head, chosen so that the rotation needs no other lane: with
-// pairs (i, i + rot/2) the two pieces are rot/2 apart.  (With one piece per lane the
-// rotation's shuffles, eight a piece, were what bounded the kernel: 75 us instead of the
-// figures below.)  A head's D <= 256 elements lie in a group of 4, 8 or 16 lanes; the sum
+// pairs (i, i + rot/2) the two pieces are rot/2 apart.  A head's D <= 256 elements lie in a group of 4, 8 or 16 lanes; the sum
 // of squares is a few shuffles inside the group.  A group walks over some heads of one
 // token, so that the token's cosines and sines and the weights are read once for them; the
 // heads ahead are on their way into shared memory meanwhile (each lane copies and reads only
 // its own pieces: no barrier).  Sums, norm and rotation are in fp32; the one rounding is the
 // store's.
+//
+// Measured (one B200): 16385 tokens of 40 heads of 128, 335 MB: 57 us, 5.9 TB/s, nine tenths of
+// what a plain copy reaches; 19 K tokens of 64 heads into a paged cache, 270 MB: 48 us.  One
+// piece per lane and four heads a group, loaded into registers, took 78 and 62 us: the
+// rotation's shuffles and the instructions spent once per group left too few loads under way.
+// Two or eight heads on their way instead of four: 61 and 61 us.
 
 #include "kd_common.cuh"
 #include "kd_ptx.cuh"
