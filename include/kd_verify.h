@@ -460,7 +460,8 @@ int kd_kv_norm_rope_write_paged(kd_bf16_t* c_pages, kd_bf16_t* r_pages, int64_t 
  *   A row without keys (nk < nq) gets out = 0 and lse = -inf.
  *   q_nope [T][H][128], q_rope [T][H][64], k_nope, v [Tk][Hk][128], k_rope [Tk][Hk][64]
  *   bf16, each with a token and a head stride in elements; k_head_stride of k_rope 0
- *   means one rope key for all heads.  q_rope and k_rope both NULL: no rope part.
+ *   means one rope key for all heads.  q_rope and k_rope both NULL: no rope part.  Without
+ *   keys (Tk = 0) their pointers may be NULL.
  *   cu_seqlens_q [B+1]; cu_seqlens_k [B+1] or NULL (the queries' own).
  *   out [T][H][128] bf16, lse [T][H] fp32, contiguous, not overlapping an input.
  * The keys and values of other sequences never enter a row, NaN or infinite ones

@@ -372,6 +372,29 @@ def test_evict_many_requests_and_long(kd):
 
 
 @pytest.mark.gpu
+def test_weights_of_a_repeated_path_entry(kd):
+    """A path that names a node twice counts its rows twice and writes its slot's weight at both places."""
+    n, H, L, cap = 5, 16, 200, 230
+    qa, qr = normal(1, n, H, 512, seed=1), normal(1, n, H, 64, seed=2)
+    c, r = normal(1, cap, 512, seed=3), normal(1, cap, 64, seed=4)
+    t = tree(n, 3)
+    vis, lse = torch.from_numpy(t[1][None].view(np.int32)).cuda(), torch.full((1, n, H), 8.0, device="cuda")
+    path = [0, 2, 2, 4]
+    w = kd.kd_kv_attn_weights(qa, qr, c, r, i32([L]), vis, lse, path=i32([path + [-1]]), length=i32([4]))
+    ref, tol = ref_weights(qa[0], qr[0], c[0, :L + n], r[0, :L + n], L, t[1], lse[0], path, None)
+    assert bool(((w[0, :L + 4].double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+def test_evict_keep_beyond_the_cache(kd):
+    c, r, w = normal(2, 50, 512, seed=1), normal(2, 50, 64, seed=2), torch.rand(2, 50, device="cuda")
+    was, lens = c.clone(), i32([50, 20])
+    kept, _, _ = kd.kd_kv_evict(c, r, lens, w, 70, 5, 5)
+    assert lens.tolist() == [50, 20] and torch.equal(c, was)
+    assert kept[0].tolist() == list(range(50)) + [-1] * 20 and kept[1].tolist() == list(range(20)) + [-1] * 50
+
+
+@pytest.mark.gpu
 def test_evict_device_errors(kd):
     Ls, cap, keep = [50, -1, 65, 40, 60], 64, 30
     c, r = normal(5, cap, 512, seed=1), normal(5, cap, 64, seed=2)

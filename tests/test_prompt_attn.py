@@ -132,6 +132,30 @@ def test_suffix_queries_and_rows_without_keys(kd, lens, klens, H, Hk, rope):
 
 
 @pytest.mark.gpu
+def test_no_keys_at_all(kd):
+    q = normal(5, 2, 192, seed=1)
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    out, lse = kd.kd_prompt_attn(q[..., :128], none, none, cu_of([2, 3]), q_rope=q[..., 128:],
+                                 k_rope=torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), cu_seqlens_k=cu_of([0, 0]))
+    assert bool((out == 0).all()) and bool(lse.isneginf().all())
+    out, lse = kd.kd_prompt_attn(q[:0, :, :128], none, none, cu_of([0]))
+    assert out.shape == (0, 2, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk", [(28, 4), (7, 1), (128, 128), (128, 1)])
+def test_groups_and_expanded_heads(kd, H, Hk):
+    """Groups that are no power of two, and keys whose heads are one head expanded (stride 0)."""
+    lens = [37, 150]
+    q, k, v, _, _ = inputs(lens, lens, H, Hk, False, seed=H)
+    out, lse = kd.kd_prompt_attn(q, k, v, cu_of(lens))
+    check(out, lse, q, k, v, lens, lens, 1.0 / math.sqrt(128.0), heads=(0, H // 2, H - 1))
+    k1, v1 = k[:, :1].expand(-1, H, -1), v[:, :1].expand(-1, H, -1)
+    out, lse = kd.kd_prompt_attn(q, k1, v1, cu_of(lens))
+    check(out, lse, q, k[:, :1], v[:, :1], lens, lens, 1.0 / math.sqrt(128.0), heads=(0, H - 1))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("big", [8.0, 40.0])
 def test_peaked_scores(kd, big):
     """Scores that climb along the keys: the running maximum moves in every tile."""

@@ -661,11 +661,10 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
                               const int32_t* cu_q, const int32_t* cu_k, int B, int T, int Tk, int H, int Hk,
                               float scale, kd_bf16_t* out, float* lse, int32_t* dev_error, cudaStream_t stream) {
   if (B < 1 || B > 65535 || T < 0 || Tk < 0 || H < 1 || H > KD_MAX_HEADS || Hk < 1 || H % Hk ||
-      !(scale > 0.f && isfinite(scale)) || (int64_t)T * H > INT32_MAX || (int64_t)Tk * Hk > INT32_MAX ||
-      (q_rope != nullptr) != (k_rope != nullptr))
+      !(scale > 0.f && isfinite(scale)) || (int64_t)T * H > INT32_MAX || (int64_t)Tk * Hk > INT32_MAX)
     return KD_EINVAL;
-  if (T == 0) return KD_OK;
-  if (!view_ok(q_nope, qnt, qnh, T) || (H > 1 && qnh == 0) || !out || (reinterpret_cast<uintptr_t>(out) & 31u) || !lse || !cu_q ||
+  if (T == 0) return KD_OK;                       // (tensors without elements may have no address)
+  if ((Tk && (q_rope != nullptr) != (k_rope != nullptr)) || !view_ok(q_nope, qnt, qnh, T) || (H > 1 && qnh == 0) || !out || (reinterpret_cast<uintptr_t>(out) & 31u) || !lse || !cu_q ||
       (Tk && (!view_ok(k_nope, knt, knh, Tk) || !view_ok(v, vt, vh, Tk))) ||
       (q_rope && (!view_ok(q_rope, qrt, qrh, T) || (H > 1 && qrh == 0) || (Tk && !view_ok(k_rope, krt, krh, Tk)))))
     return KD_EINVAL;
