@@ -14,8 +14,8 @@
 // its own pieces: no barrier).  Sums, norm and rotation are in fp32; the one rounding is the
 // store's.
 //
-// Measured (one B200): 16385 tokens of 40 heads of 128, 335 MB: 57 us, 5.9 TB/s, nine tenths of
-// what a plain copy reaches; 19 K tokens of 64 heads into a paged cache, 270 MB: 48 us.  One
+// Measured (one B200): 16385 tokens of 40 heads of 128, 344 MB: 57 us, 5.9 TB/s, nine tenths of
+// what a plain copy reaches; 14.3 K tokens of 64 heads into a paged cache, 271 MB: 48 us.  One
 // piece per lane and four heads a group, loaded into registers, took 78 and 62 us: the
 // rotation's shuffles and the instructions spent once per group left too few loads under way.
 // Two or eight heads on their way instead of four: 61 and 61 us.

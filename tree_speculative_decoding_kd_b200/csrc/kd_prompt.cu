@@ -36,7 +36,7 @@
 //
 // Measured (one B200, calls behind each other; the longer two at the 1000 W cap, 1.4 to 1.6
 // GHz): one prompt of 16384 tokens, 16 query heads on 2 key heads of 128: 1000 us (1.10
-// PFLOP/s, 1.29 in a call by itself); 4 prompts of 900 to 3100 tokens, 64 heads of 192/128: 600
+// PFLOP/s, 1.29 in a call by itself); 4 prompts of 2000 to 3070 tokens, 64 heads of 192/128: 600
 // us (0.92, 1.11); 32 prompts of 1 to 300 tokens, 64 heads of 192/128: 86 us, where its inputs
 // and outputs are 352 MB, 54 us.  What bounds it: the chain of one tile (scores, maximum,
 // exponentials, the two products' hand-overs, about 2900 cycles a key tile where the products
