@@ -565,6 +565,23 @@ int kd_kv_evict_paged(const kd_bf16_t* c_pages, const kd_bf16_t* r_pages, int64_
                       cudaStream_t stream);
 
 /*
+ * kd_call_packed -- any of the calls above from kd_qk_norm_rope on, its arguments as `count`
+ * consecutive 8-byte values in their order (args is a HOST pointer, read before the call
+ * returns): integers and pointers as int64, floats as double.  For bindings that pay for every
+ * argument they convert.  KD_EINVAL for an unknown op, another count than the call has
+ * parameters, or an integer that does not fit its parameter; else what the call returns.
+ */
+#define KD_OP_QK_NORM_ROPE              0
+#define KD_OP_KV_NORM_ROPE_WRITE        1
+#define KD_OP_KV_NORM_ROPE_WRITE_PAGED  2
+#define KD_OP_PROMPT_ATTN               3
+#define KD_OP_KV_ATTN_WEIGHTS           4
+#define KD_OP_KV_ATTN_WEIGHTS_PAGED     5
+#define KD_OP_KV_EVICT                  6
+#define KD_OP_KV_EVICT_PAGED            7
+int kd_call_packed(int op, const int64_t* args, int count);
+
+/*
  * kd_read_device_error -- synchronises `stream`, returns the device error word
  * (>= 0, KD_DEV_* bits) and zeroes it when `clear` is non-zero.  Negative return =
  * KD_E* code of the copy itself.

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libkdverify.so")
 TRACE_LIB = os.path.join(PKG, "libkdverify_trace.so")
 
 SOURCES = ["kd_tree.cu", "kd_attn_simt.cu", "kd_attn_tc.cu", "kd_argmax.cu", "kd_tree_build.cu",
-           "kd_norm_rope.cu", "kd_prompt.cu", "kd_attn_weights.cu", "kd_evict.cu"]
+           "kd_norm_rope.cu", "kd_prompt.cu", "kd_attn_weights.cu", "kd_evict.cu", "kd_packed.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]

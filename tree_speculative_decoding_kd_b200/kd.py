@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -63,6 +64,7 @@ _SIGS = {
                          _p, _p, _p, _p]),
     "kd_kv_evict_paged": (_i, [_p, _p, _i64, _i64, _i, _p, _i64, _i64, _p, _p, _i64, _i, _i, _i, _i, _p, _p, _i64,
                                _i64, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p]),
+    "kd_call_packed": (_i, [_i, ctypes.c_char_p, _i]),
     "kd_read_device_error": (_i, [_p, _i, _p]),
     "kd_strerror": (ctypes.c_char_p, [_i]),
 }
@@ -70,6 +72,24 @@ for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
     _fn.restype = _res
     _fn.argtypes = _args
+
+# Calls made through kd_call_packed, in the order of their op codes.
+_PACKED = ("kd_qk_norm_rope", "kd_kv_norm_rope_write", "kd_kv_norm_rope_write_paged", "kd_prompt_attn",
+           "kd_kv_attn_weights", "kd_kv_attn_weights_paged", "kd_kv_evict", "kd_kv_evict_paged")
+
+
+def _packed(name):
+    """The call `name` with its arguments (integers, addresses with 0 for none, floats) packed into
+    one buffer: converting them one by one costs ctypes more than the launch of a small call."""
+    op, types = _PACKED.index(name), _SIGS[name][1]
+    pack, count = struct.Struct("".join("d" if t is _f else "q" for t in types)).pack, len(types)
+
+    def call(*args):
+        rc = lib.kd_call_packed(op, pack(*args), count)
+        if rc:
+            _check(rc, name)
+    return call
+
 
 D_C, D_R = 512, 64
 KD_DEV_BITS = {0x01: "BAD_PARENT", 0x02: "CACHE_FULL", 0x04: "BAD_PATH",
@@ -98,6 +118,10 @@ def _stream_of(stream, device) -> int:
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _need(t, dtype, name, contiguous=True):
@@ -386,6 +410,16 @@ def kd_kv_compact_paged(c_pages, r_pages, page_table, page_size, path, length, c
 
 
 # ------------------------------------------------------------------ operators next to the verify step
+_call_qk_norm_rope = _packed("kd_qk_norm_rope")
+_call_kv_norm_rope_write = _packed("kd_kv_norm_rope_write")
+_call_kv_norm_rope_write_paged = _packed("kd_kv_norm_rope_write_paged")
+_call_prompt_attn = _packed("kd_prompt_attn")
+_call_kv_attn_weights = _packed("kd_kv_attn_weights")
+_call_kv_attn_weights_paged = _packed("kd_kv_attn_weights_paged")
+_call_kv_evict = _packed("kd_kv_evict")
+_call_kv_evict_paged = _packed("kd_kv_evict_paged")
+
+
 def _on_device(*tensors) -> int:
     """Index of the current CUDA device, on which every tensor given (None skipped) has to lie."""
     dev = None
@@ -489,10 +523,9 @@ def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, e
         if k_out is None:
             k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=q.device)
         _, _, _, kot, koh = _heads(k_out, "k_out", T, Hk, D)
-    _check(lib.kd_qk_norm_rope(q.data_ptr(), qt, qh, _ptr(k), kt, kh, _ptr(q_weight), _ptr(k_weight), eps,
-                               rope_table.data_ptr(), max_pos, positions.data_ptr(), T, H, Hk, D, rot, rot_offset,
-                               interleaved, q_out.data_ptr(), qot, qoh, _ptr(k_out), kot, koh, _ptr(dev_error),
-                               _stream_of(stream, dev)), "kd_qk_norm_rope")
+    _call_qk_norm_rope(q.data_ptr(), qt, qh, _addr(k), kt, kh, _addr(q_weight), _addr(k_weight), eps,
+        rope_table.data_ptr(), max_pos, positions.data_ptr(), T, H, Hk, D, rot, rot_offset, interleaved,
+        q_out.data_ptr(), qot, qoh, _addr(k_out), kot, koh, _addr(dev_error), _stream_of(stream, dev))
     return q_out, k_out
 
 
@@ -539,10 +572,10 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
                                                        q_rope_in, q_rope_out)
     if rows != B:
         raise ValueError("the cache must hold B requests")
-    _check(lib.kd_kv_norm_rope_write(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(kv), kv.stride(0),
-                                     _ptr(kv_weight), eps, _ptr(rope_table), max_pos, _ptr(positions),
-                                     interleaved, _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H,
-                                     _ptr(q_rope_out), _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_norm_rope_write")
+    _call_kv_norm_rope_write(c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap, cache_lens.data_ptr(), kv.data_ptr(),
+        kv.stride(0), _addr(kv_weight), eps, rope_table.data_ptr(), max_pos, _addr(positions), interleaved,
+        _addr(cu_seqlens), B, T, _addr(q_rope_in), qt, qh, H, _addr(q_rope_out), _addr(dev_error),
+        _stream_of(stream, dev))
     return q_rope_out
 
 
@@ -555,11 +588,10 @@ def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_l
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
                                                        q_rope_in, q_rope_out)
     sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, B)
-    _check(lib.kd_kv_norm_rope_write_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
-                                           _ptr(cache_lens), _ptr(kv), kv.stride(0), _ptr(kv_weight), eps,
-                                           _ptr(rope_table), max_pos, _ptr(positions), interleaved,
-                                           _ptr(cu_seqlens), B, T, _ptr(q_rope_in), qt, qh, H, _ptr(q_rope_out),
-                                           _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_norm_rope_write_paged")
+    _call_kv_norm_rope_write_paged(c_pages.data_ptr(), r_pages.data_ptr(), sc, sr, int(page_size),
+        page_table.data_ptr(), M, N, cache_lens.data_ptr(), kv.data_ptr(), kv.stride(0), _addr(kv_weight), eps,
+        rope_table.data_ptr(), max_pos, _addr(positions), interleaved, _addr(cu_seqlens), B, T, _addr(q_rope_in), qt,
+        qh, H, _addr(q_rope_out), _addr(dev_error), _stream_of(stream, dev))
     return q_rope_out
 
 
@@ -598,9 +630,9 @@ def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu
         lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
     _typed(out, torch.bfloat16, "out", (T, H, 128))
     _typed(lse, torch.float32, "lse", (T, H))
-    _check(lib.kd_prompt_attn(_ptr(q_nope), qnt, qnh, _ptr(q_rope), qrt, qrh, _ptr(k_nope), knt, knh, _ptr(k_rope),
-                              krt, krh, _ptr(v), vt, vh, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, T, Tk, H, Hk,
-                              scale, _ptr(out), _ptr(lse), _ptr(dev_error), _stream_of(stream, dev)), "kd_prompt_attn")
+    _call_prompt_attn(q_nope.data_ptr(), qnt, qnh, _addr(q_rope), qrt, qrh, k_nope.data_ptr(), knt, knh,
+        _addr(k_rope), krt, krh, v.data_ptr(), vt, vh, cu_seqlens_q.data_ptr(), _addr(cu_seqlens_k), B, T, Tk, H, Hk,
+        scale, out.data_ptr(), lse.data_ptr(), _addr(dev_error), _stream_of(stream, dev))
     return out, lse
 
 
@@ -644,9 +676,9 @@ def kd_kv_attn_weights(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path=N
                                                  weights_out, cap)
     if rows != B:
         raise ValueError("the cache must hold B requests")
-    _check(lib.kd_kv_attn_weights(_ptr(q_abs), _ptr(q_rope), _ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens),
-                                  _ptr(vis), _ptr(lse), _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
-                                  _ptr(weights_out), wo, _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_attn_weights")
+    _call_kv_attn_weights(q_abs.data_ptr(), q_rope.data_ptr(), c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap,
+        cache_lens.data_ptr(), vis.data_ptr(), lse.data_ptr(), _addr(path), _addr(length), B, n, H, scale,
+        _addr(weights_in), wi, weights_out.data_ptr(), wo, _addr(dev_error), _stream_of(stream, dev))
     return weights_out
 
 
@@ -659,11 +691,10 @@ def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_s
     sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, cache_lens.shape[0])
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
                                                  weights_out, M * page_size)
-    _check(lib.kd_kv_attn_weights_paged(_ptr(q_abs), _ptr(q_rope), _ptr(c_pages), _ptr(r_pages), sc, sr,
-                                        int(page_size), _ptr(page_table), M, N, _ptr(cache_lens), _ptr(vis), _ptr(lse),
-                                        _ptr(path), _ptr(length), B, n, H, scale, _ptr(weights_in), wi,
-                                        _ptr(weights_out), wo, _ptr(dev_error), _stream_of(stream, dev)),
-           "kd_kv_attn_weights_paged")
+    _call_kv_attn_weights_paged(q_abs.data_ptr(), q_rope.data_ptr(), c_pages.data_ptr(), r_pages.data_ptr(), sc, sr,
+        int(page_size), page_table.data_ptr(), M, N, cache_lens.data_ptr(), vis.data_ptr(), lse.data_ptr(),
+        _addr(path), _addr(length), B, n, H, scale, _addr(weights_in), wi, weights_out.data_ptr(), wo,
+        _addr(dev_error), _stream_of(stream, dev))
     return weights_out
 
 
@@ -702,9 +733,9 @@ def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_
                                                          lens_out, kept)
     if rows != B or drows != B:
         raise ValueError("the caches must hold B requests")
-    _check(lib.kd_kv_evict(_ptr(c_kv), _ptr(k_rope), sc, sr, cap, _ptr(cache_lens), _ptr(weights_in), wi, int(keep),
-                           int(sink), int(recent), B, _ptr(c_dst), _ptr(r_dst), dc, dr, dcap, _ptr(weights_out), wo,
-                           _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_evict")
+    _call_kv_evict(c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap, cache_lens.data_ptr(), weights_in.data_ptr(), wi,
+        int(keep), int(sink), int(recent), B, c_dst.data_ptr(), r_dst.data_ptr(), dc, dr, dcap,
+        weights_out.data_ptr(), wo, lens_out.data_ptr(), kept.data_ptr(), _addr(dev_error), _stream_of(stream, dev))
     return kept, weights_out, lens_out
 
 
@@ -727,10 +758,10 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
     dc, dr, DM, DN = _pages(c_dst, r_dst, dst_page_table, page_size, cache_lens.shape[0])
     B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, M * page_size, DM * page_size, keep,
                                                          inplace, weights_out, lens_out, kept)
-    _check(lib.kd_kv_evict_paged(_ptr(c_pages), _ptr(r_pages), sc, sr, int(page_size), _ptr(page_table), M, N,
-                                 _ptr(cache_lens), _ptr(weights_in), wi, int(keep), int(sink), int(recent), B,
-                                 _ptr(c_dst), _ptr(r_dst), dc, dr, _ptr(dst_page_table), DM, DN, _ptr(weights_out), wo,
-                                 _ptr(lens_out), _ptr(kept), _ptr(dev_error), _stream_of(stream, dev)), "kd_kv_evict_paged")
+    _call_kv_evict_paged(c_pages.data_ptr(), r_pages.data_ptr(), sc, sr, int(page_size), page_table.data_ptr(), M, N,
+        cache_lens.data_ptr(), weights_in.data_ptr(), wi, int(keep), int(sink), int(recent), B, c_dst.data_ptr(),
+        r_dst.data_ptr(), dc, dr, dst_page_table.data_ptr(), DM, DN, weights_out.data_ptr(), wo, lens_out.data_ptr(),
+        kept.data_ptr(), _addr(dev_error), _stream_of(stream, dev))
     return kept, weights_out, lens_out
 
 
