@@ -195,6 +195,38 @@ def test_heads_bad_position_zero_rows_and_large_values(kd):
     assert e.shape == (0, H, D)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,Hk,D,rot,off,inter", [
+    (40003, 1, 1, 192, 32, 160, True), (30001, 3, 0, 64, 64, 0, False), (9001, 7, 2, 128, 48, 16, False),
+    (5003, 20, 3, 72, 16, 8, True), (2501, 9, 5, 256, 240, 0, False), (20011, 1, 3, 16, 16, 0, True)])
+def test_heads_of_many_tokens_in_a_row(kd, T, H, Hk, D, rot, off, inter):
+    """Head counts that leave a run of heads to several tokens: the tokens' own angles, a token of
+    a bad position between good ones left as it was, and the same values in place."""
+    qkv = normal(T, H + 2 * Hk + 1, D, seed=T)
+    q, k = qkv[:, :H], qkv[:, H:H + Hk] if Hk else None
+    table, qw, kw = table_of(700, rot), normal(D, seed=1), normal(D, seed=2)
+    pos = torch.randint(0, 700, (T,), device="cuda", dtype=torch.int32)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[5::97] = True
+    bad[T - 1] = bad[1000:1020] = True
+    pos[bad] = torch.where(torch.arange(int(bad.sum()), device="cuda") % 2 == 0, -1, 700).int()
+    outs = [torch.full_like(q, 7.0), None if k is None else torch.full_like(k, 7.0)]
+    err = kd.new_error_word()
+    args = dict(q_weight=qw, k_weight=kw if Hk else None, eps=EPS, rot_offset=off, interleaved=inter)
+    kd.kd_qk_norm_rope(q, k, pos, table, q_out=outs[0], k_out=outs[1], dev_error=err, **args)
+    assert kd.decode_device_error(kd.kd_read_device_error(err)) == ["BAD_POSITION"]
+    was = qkv.clone()
+    kd.kd_qk_norm_rope(q, k, pos, table, q_out=q, k_out=k, **args)
+    for x, y, w, got in ((was[:, :H], q, qw, outs[0]), (was[:, H:H + Hk], k, kw, outs[1])):
+        if got is None:
+            continue
+        normed, ref = ref_heads(x[~bad], w, pos[~bad], table, off, inter)
+        within(got[~bad], ref, normed)
+        assert bool((got[bad] == 7.0).all())
+        assert torch.equal(y[~bad], got[~bad]) and torch.equal(y[bad], x[bad])
+    assert torch.equal(qkv[:, H + Hk:], was[:, H + Hk:])
+
+
 # ------------------------------------------------------------------ into the cache
 def cache(kd, B, cap, page, wide, seed):
     """c, r, page table, rows of every slot [B][cap]; `wide`: one 576-wide interleaved buffer."""

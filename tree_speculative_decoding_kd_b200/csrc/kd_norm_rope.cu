@@ -8,10 +8,10 @@
 // read once and written once, 16 bytes at a time.  A lane holds two pieces of eight
 // neighbouring elements of a head, chosen so that the rotation needs no other lane: with
 // pairs (i, i + rot/2) the two pieces are rot/2 apart.  A head's D <= 256 elements lie in a group of 4, 8 or 16 lanes; the sum
-// of squares is a few shuffles inside the group.  A group walks over some heads of one
-// token, so that the token's cosines and sines and the weights are read once for them; the
-// heads ahead are on their way into shared memory meanwhile (each lane copies and reads only
-// its own pieces: no barrier).  Sums, norm and rotation are in fp32; the one rounding is the
+// of squares is a few shuffles inside the group.  A group walks over up to eight heads, of
+// one token where that fills it, so that the token's cosines and sines and the weights are
+// read once for them; the heads ahead are on their way into shared memory meanwhile (each
+// lane copies and reads only its own pieces: no barrier).  Sums, norm and rotation are in fp32; the one rounding is the
 // store's.
 //
 // Measured (one B200): 16385 tokens of 40 heads of 128, 344 MB: 57 us, 5.9 TB/s, nine tenths of
@@ -101,7 +101,8 @@ struct QkSide {
   const uint16_t* w;
   uint16_t* out;
   int64_t it, ih, ot, oh;      // token and head strides, in and out
-  int heads, items;            // items = ceil(heads / per) groups per token
+  int heads;
+  unsigned groups;             // of `per` heads in a row, counted over all tokens
 };
 struct QkParams {
   QkSide q, k;
@@ -115,28 +116,28 @@ struct QkParams {
 
 // G lanes per head (the least power of two that holds D / 16).  Lane l of a group has
 //   l < rot / 16: elements off + 8 l and off + rot / 2 + 8 l, eight each: both halves of pairs;
-//   else: the elements outside the rotated range, sixteen in a row of those, the last lane maybe eight.
-template <int G>
+//   else: one piece of each half of those outside the rotated range (neighbouring lanes have
+//         neighbouring pieces: two pieces in a row per lane, half of each 32-byte sector at a time,
+//         took 70 us where this takes 60, 20000 tokens of 32 heads of 128, half of each rotated).
+//
+// A group has `per` heads in a row, counted over all tokens.  SPAN: they may be of several tokens,
+// whose angles are then loaded as the group comes to them.
+template <int G, bool SPAN>
 __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkParams p) {
   __shared__ uint4 pieces[DEPTH * 2 * THREADS];
   const Ring ring(pieces);
   const int lane = threadIdx.x & (G - 1);
-  const unsigned items = (unsigned)(p.q.items + p.k.items);
   const unsigned g = blockIdx.x * (THREADS / G) + threadIdx.x / G;
-  unsigned t = g / items, item = g - t * items;
-  bool live = t < (unsigned)p.T;                   // no early exit: the shuffles take whole warps
-  int64_t at = 0;
-  if (live) {
-    at = p.pos[t];
-    if (at < 0 || at >= p.max_pos) {
-      if (lane == 0) raise_dev_error(p.err, KD_DEV_BAD_POSITION);
-      live = false;
-    }
-  }
-  const bool is_k = item >= (unsigned)p.q.items;
+  const bool is_k = g >= p.q.groups;
   const QkSide& s = is_k ? p.k : p.q;
-  const int h0 = (int)(is_k ? item - p.q.items : item) * p.per, n = live ? min(p.per, s.heads - h0) : 0;
-  const int rest = (p.D - p.rot) >> 3, r0 = 2 * (lane - (p.rot >> 4));     // pieces outside the range, this lane's first
+  // the group's heads: n, from head h of token t on
+  const unsigned heads = (unsigned)s.heads, f0 = (is_k ? g - p.q.groups : g) * (unsigned)p.per;
+  const unsigned all = (unsigned)p.T * heads;
+  const int n = f0 < all ? (int)min((unsigned)p.per, all - f0) : 0;    // no early exit: the shuffles take whole warps
+  unsigned t = n ? f0 / heads : 0u;
+  const unsigned h = n ? f0 - t * heads : 0u;
+  const int rest = (p.D - p.rot) >> 3;               // pieces outside the range; this lane's:
+  const int r0 = lane - (p.rot >> 4), r1 = r0 + ((rest + 1) >> 1);
   const bool rotated = r0 < 0;
   int ea, eb;
   if (rotated) {
@@ -144,43 +145,60 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkParams p)
     eb = ea + (p.rot >> 1);
   } else {
     ea = 8 * r0 < p.off ? 8 * r0 : 8 * r0 + p.rot;
-    eb = 8 * (r0 + 1) < p.off ? 8 * (r0 + 1) : 8 * (r0 + 1) + p.rot;
+    eb = 8 * r1 < p.off ? 8 * r1 : 8 * r1 + p.rot;
   }
-  const bool has_a = r0 < rest, has_b = rotated || r0 + 1 < rest;
-  const uint16_t* in = s.in + (int64_t)t * s.it + h0 * s.ih;
-  uint16_t* out = s.out + (int64_t)t * s.ot + h0 * s.oh;
-  auto ask = [&](int h) {
-    if (h < n) {
-      ring.copy(h & (DEPTH - 1), 0, in + (has_a ? h * s.ih + ea : 0), has_a);
-      ring.copy(h & (DEPTH - 1), 1, in + (has_b ? h * s.ih + eb : 0), has_b);
+  const bool has_a = rotated || 2 * r0 < rest, has_b = rotated || (has_a && r1 < rest);
+  const uint16_t* in = s.in + (int64_t)t * s.it + h * s.ih;
+  uint16_t* out = s.out + (int64_t)t * s.ot + h * s.oh;
+  int left = (int)(heads - h), left_in = left;       // heads of the token that are left, to store and to ask for
+  const int64_t wrap_in = s.it - (heads - 1) * s.ih, wrap_out = s.ot - (heads - 1) * s.oh;
+  auto ask = [&](int i) {
+    if (i < n) {
+      ring.copy(i & (DEPTH - 1), 0, in + (has_a ? ea : 0), has_a);
+      ring.copy(i & (DEPTH - 1), 1, in + (has_b ? eb : 0), has_b);
+      if (SPAN && --left_in == 0) {
+        in += wrap_in;
+        left_in = (int)heads;
+      } else {
+        in += s.ih;
+      }
     }
     Ring::commit();
   };
+  const int pos = n ? p.pos[t] : 0;
+  int next = SPAN && left < n ? p.pos[t + 1] : 0;    // position of the token after this one
 #pragma unroll
-  for (int h = 0; h < DEPTH; ++h) ask(h);
+  for (int i = 0; i < DEPTH; ++i) ask(i);
   const bool norm = s.w != nullptr;
   float wa[8], wb[8];
-  if (norm && live) {
+  if (norm && n) {
     unpack8(has_a ? __ldg(reinterpret_cast<const uint4*>(s.w + ea)) : make_uint4(0, 0, 0, 0), wa);
     unpack8(has_b ? __ldg(reinterpret_cast<const uint4*>(s.w + eb)) : make_uint4(0, 0, 0, 0), wb);
   }
+  // a token's angles; false when its position is bad
+  auto turn_of = [&](Turn& turn, int64_t at) -> bool {
+    const bool good = at >= 0 && at < p.max_pos;
+    if (!good && lane == 0) raise_dev_error(p.err, KD_DEV_BAD_POSITION);
+    turn.load(p.table + at * p.rot, ea - p.off, eb - p.off, p.rot, good && rotated, p.inter != 0);
+    return good;
+  };
   Turn turn;
-  turn.load(p.table + at * p.rot, ea - p.off, eb - p.off, p.rot, live && rotated, p.inter != 0);
+  bool live = n && turn_of(turn, pos);
 
   // the groups of a warp may have fewer heads or none: the shuffles are for all
   const int most = __reduce_max_sync(0xffffffffu, n);
 #pragma unroll 1
-  for (int h = 0; h < most; ++h) {
+  for (int i = 0; i < most; ++i) {
     Ring::wait();
     float a[8], b[8];
-    unpack8(ptx::ld_shared_v4(ring.piece(h & (DEPTH - 1), 0)), a);
-    unpack8(ptx::ld_shared_v4(ring.piece(h & (DEPTH - 1), 1)), b);
-    ask(h + DEPTH);
+    unpack8(ptx::ld_shared_v4(ring.piece(i & (DEPTH - 1), 0)), a);
+    unpack8(ptx::ld_shared_v4(ring.piece(i & (DEPTH - 1), 1)), b);
+    ask(i + DEPTH);
     float ss = 0.f, sb = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ss += a[i] * a[i];
-      sb += b[i] * b[i];
+    for (int e = 0; e < 8; ++e) {
+      ss += a[e] * a[e];
+      sb += b[e] * b[e];
     }
     ss += sb;
 #pragma unroll
@@ -188,17 +206,27 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkParams p)
     if (norm) {
       const float r = rsqrtf(ss * p.inv_d + p.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = a[i] * r * wa[i];
-        b[i] = b[i] * r * wb[i];
+      for (int e = 0; e < 8; ++e) {
+        a[e] = a[e] * r * wa[e];
+        b[e] = b[e] * r * wb[e];
       }
     }
     turn.apply(a, b);
-    if (h < n) {
+    if (i < n && live) {
       if (has_a) *reinterpret_cast<uint4*>(out + ea) = pack8(a);
       if (has_b) *reinterpret_cast<uint4*>(out + eb) = pack8(b);
     }
-    out += s.oh;
+    if (SPAN && --left == 0) {                       // the next token
+      out += wrap_out;
+      left = (int)heads;
+      ++t;
+      if (i + 1 < n) {
+        live = turn_of(turn, next);
+        if (i + 1 + (int)heads < n) next = p.pos[t + 1];
+      }
+    } else {
+      out += s.oh;
+    }
   }
 }
 
@@ -368,11 +396,11 @@ extern "C" int kd_qk_norm_rope(const kd_bf16_t* q, int64_t qt, int64_t qh, const
   const int G = D <= 64 ? 4 : D <= 128 ? 8 : 16;
   // heads of a group: as many as leave every SM about 1024 lanes of work, at most 8
   int per = 8;
-  while (per > 1 && (int64_t)T * ((H + per - 1) / per + (Hk + per - 1) / per) * G < (int64_t)sms * 1024) per /= 2;
+  while (per > 1 && (int64_t)T * (H + Hk) / per * G < (int64_t)sms * 1024) per /= 2;
   nr::QkParams p;
   p.per = per;
-  p.q = {q, q_weight, q_out, qt, qh, qot, qoh, H, (H + per - 1) / per};
-  p.k = {k, k_weight, k_out, kt, kh, kot, koh, Hk, (Hk + per - 1) / per};
+  p.q = {q, q_weight, q_out, qt, qh, qot, qoh, H, (unsigned)(((int64_t)T * H + per - 1) / per)};
+  p.k = {k, k_weight, k_out, kt, kh, kot, koh, Hk, (unsigned)(((int64_t)T * Hk + per - 1) / per)};
   p.table = rope_table;
   p.pos = positions;
   p.err = dev_error;
@@ -384,11 +412,16 @@ extern "C" int kd_qk_norm_rope(const kd_bf16_t* q, int64_t qt, int64_t qh, const
   p.rot = rot;
   p.off = rot_offset;
   p.inter = interleaved;
-  const int64_t groups = (int64_t)T * (p.q.items + p.k.items);
+  const int64_t groups = (int64_t)p.q.groups + p.k.groups;
   const unsigned grid = (unsigned)((groups * G + nr::THREADS - 1) / nr::THREADS);
-  if (G == 4) nr::qk_norm_rope_kernel<4><<<grid, nr::THREADS, 0, stream>>>(p);
-  else if (G == 8) nr::qk_norm_rope_kernel<8><<<grid, nr::THREADS, 0, stream>>>(p);
-  else nr::qk_norm_rope_kernel<16><<<grid, nr::THREADS, 0, stream>>>(p);
+  // Groups stay inside a token where that leaves none of them short, else they span tokens:
+  // 116186 tokens of 1 + 1 heads of 192 56 us against 78 inside, 30000 of 14 + 2 heads of 128 50
+  // against 53; 16385 tokens of 32 + 8 heads 60 against 57, 20000 of 16 + 16 of 192 107 against 92.
+  const bool span = H % per || Hk % per;
+  const auto go = [&](auto inside, auto spanning) { (span ? spanning : inside)<<<grid, nr::THREADS, 0, stream>>>(p); };
+  if (G == 4) go(nr::qk_norm_rope_kernel<4, false>, nr::qk_norm_rope_kernel<4, true>);
+  else if (G == 8) go(nr::qk_norm_rope_kernel<8, false>, nr::qk_norm_rope_kernel<8, true>);
+  else go(nr::qk_norm_rope_kernel<16, false>, nr::qk_norm_rope_kernel<16, true>);
   return launch_status("qk_norm_rope_kernel");
 }
 
