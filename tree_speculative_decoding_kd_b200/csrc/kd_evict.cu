@@ -5,9 +5,12 @@
 // the last slot that is kept, by a radix selection over order-preserving 32-bit keys (11 +
 // 11 + 10 bits, a histogram in shared memory each, added up across the cluster through
 // distributed shared memory), and then walks the slots in order once, numbering the kept
-// ones: equal weights are taken from the lowest slot.  It is bound by latency: about 19 us,
+// ones: equal weights are taken from the lowest slot.  It is bound by latency: about 17 us,
 // 4 for each pass (histogram 0.8, cluster barrier 0.9, 57 KB of the others' histograms 1 to 2,
-// scan 0.5) and 5 for the numbering.  One CTA per request took 66 us for 32 K slots.
+// scan 0.3) and 4 for the numbering; where a pass ends on a digit whose keys are all kept, the
+// rest is left out (64 requests without equal weights: 76 to 73 us with the move).  1024
+// threads of 32 registers and four slots each took 2 us more, one CTA per request 66 us for
+// 32 K slots; rows already known to be kept prefetched into L2 during the passes cost 4 to 20.
 // The move copies the kept rows: bound by memory, 2 x 1152 bytes a row, 16 bytes per lane: 302
 // MB in 54 us, 5.6 TB/s.  It is launched with the selection still running (programmatic
 // dependent launch) and waits for it on the device.
@@ -19,9 +22,9 @@
 namespace kd {
 namespace ev {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 2048;
-constexpr int PER = 4;                       // neighbouring slots a thread numbers per step
+constexpr int PER = 8;                       // neighbouring slots a thread numbers per step
 constexpr int CHUNK = THREADS * PER;         // slots a CTA works on per step
 constexpr int MAXC = 8;                      // CTAs of a cluster
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
   }
   if (lane == 31) warp_sums[w] = v;
   __syncthreads();
-  uint32_t s = warp_sums[lane];
+  uint32_t s = lane < WARPS ? warp_sums[lane] : 0u;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t o = __shfl_up_sync(0xffffffffu, s, d);
@@ -70,9 +73,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
@@ -80,7 +84,7 @@ __device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
 __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p, const int cs) {
   __shared__ __align__(16) uint32_t hist[3][BINS];
   __shared__ uint32_t warp_sums[WARPS];
-  __shared__ uint32_t found[2], totals[2];
+  __shared__ uint32_t found[3], totals[2];
   asm volatile("griddepcontrol.launch_dependents;");      // the move may come up and wait
   const int b = blockIdx.x / cs, tid = threadIdx.x;
   const int rank = cs > 1 ? (int)ptx::cluster_ctarank() : 0;
@@ -117,12 +121,11 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p
     }
   };
   load(0);
-  uint32_t thr = 0, need = 0;                          // keys above thr are kept, and `need` equal to it
+  uint32_t thr = 0, need = 0, mask = 0;                // keys whose bits of mask are above thr are kept, `need` equal to it
   if (L > p.keep && p.keep > p.sink + p.recent) {
     need = (uint32_t)(p.keep - p.sink - p.recent);
     for (int i = tid; i < 3 * BINS; i += THREADS) (&hist[0][0])[i] = 0u;
     __syncthreads();
-    uint32_t mask = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
@@ -143,26 +146,31 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p
       } else {
         __syncthreads();
       }
-      // thread t holds the bins 2047 - 2t and 2046 - 2t: sums run from the largest digit
-      const uint32_t* mine = &hist[pass][BINS - 2 - 2 * tid];
-      uint32_t h0 = mine[0], h1 = mine[1];
-      for (int r = 1; r < cs; ++r) {                   // the others', from the next one on
+      // thread t holds the bins 2047 - 4t to 2044 - 4t: sums run from the largest digit
+      const uint32_t at = ptx::smem_u32(&hist[pass][BINS - 4 - 4 * tid]);
+      uint32_t h[4] = {0u, 0u, 0u, 0u};                // of the largest digit first
+      for (int r = 0; r < cs; ++r) {                   // the others', from the next one on
         const int q = rank + r < cs ? rank + r : rank + r - cs;
-        const uint2 o = ld_cluster_v2(ptx::map_to_rank(ptx::smem_u32(mine), (uint32_t)q));
-        h0 += o.x;
-        h1 += o.y;
+        const uint4 o = cs > 1 ? ld_cluster_v4(ptx::map_to_rank(at, (uint32_t)q)) : ptx::ld_shared_v4(at);
+        h[0] += o.w, h[1] += o.z, h[2] += o.y, h[3] += o.x;
       }
       uint32_t total;
-      const uint32_t upto = block_scan(h1 + h0, warp_sums, total), above = upto - h1 - h0;
-      if (above < need && upto >= need) {
-        const bool hi = above + h1 >= need;
-        found[0] = (uint32_t)(hi ? BINS - 1 - 2 * tid : BINS - 2 - 2 * tid);
-        found[1] = need - (hi ? above : above + h1);
+      const uint32_t mine = (h[0] + h[1]) + (h[2] + h[3]);
+      uint32_t above = block_scan(mine, warp_sums, total) - mine;
+      if (above < need && above + mine >= need) {
+        int i = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (i == k && above + h[k] < need) above += h[k], i = k + 1;
+        found[0] = (uint32_t)(BINS - 1 - 4 * tid - i);
+        found[1] = need - above;
+        found[2] = i == 0 ? h[0] : i == 1 ? h[1] : i == 2 ? h[2] : h[3];
       }
       __syncthreads();
       thr |= found[0] << shift;
       need = found[1];
       mask |= digits << shift;
+      if (found[2] == need) break;                     // every key of the digit is kept: the rest does not matter
     }
   }
   const bool all = L <= p.keep, none = !all && p.keep == p.sink + p.recent;
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p
       const int j = at0 + i;
       kind[i] = 0;
       if (j < L) {
-        const uint32_t key = order_key(v[i]);
+        const uint32_t key = order_key(v[i]) & mask;
         if (all || j < first || j >= last || (!none && key > thr)) kind[i] = 1u << 16;
         else if (!none && key == thr) kind[i] = 1u;
       }
