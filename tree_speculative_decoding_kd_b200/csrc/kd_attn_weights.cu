@@ -291,7 +291,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
           const int nodes = min(p.per_tile, cur.count - (pr + t * pairs) * p.per_tile);
           const uint32_t idesc = idesc_bf16(UK, 2 * ((nodes + 1) >> 1) * p.Hp, 0, 0);
           const uint32_t sb = s % NS, d = tmem + sb * BN;
-          if (!(ok = pipe.wait_remote(S_FREE + sb, ((s / NS) & 1u) ^ 1u))) break;
+          if (!(ok = pipe.wait(S_FREE + sb, ((s / NS) & 1u) ^ 1u))) break;
           tc_fence_after();
           for (int c = 0; c < NCH; ++c, ++q) {
             const uint32_t st = q % NQ;
@@ -379,7 +379,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
       for (int t = pr; t < cur.tiles; t += pairs, ++ts) {
         const uint32_t sb = ts % NS, par = (ts / NS) & 1u;
         const int rows = min(p.per_tile, cur.count - t * p.per_tile) * p.Hp;
-        ok = pipe.wait(Z_FULL + sb, par) && pipe.wait_remote(S_FULL + sb, par);
+        ok = pipe.wait(Z_FULL + sb, par) && pipe.wait(S_FULL + sb, par);
         if (named_bar_red_or(1, 256, !ok)) {
           ok = false;
           break;
@@ -430,7 +430,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(pipe.bar(Z_FREE + sb));
-          mbar_arrive_remote(even(S_FREE + sb));
+          mbar_arrive_remote_tmem(even(S_FREE + sb));
         }
       }
       if (!ok) break;
