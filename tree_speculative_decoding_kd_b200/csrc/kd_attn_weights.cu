@@ -14,8 +14,9 @@
 // the query rows pass through four.  A chunk of keys is refilled for the next unit as soon as
 // the last query tile has used it, so that with few rows (one query tile, as for an accepted
 // path: bound by the cache's bytes) the next unit's keys stream in behind this one's products.
-// Measured (one B200): 4 x 16384 keys against 8192 rows 500 us (1.25 PFLOP/s at the power
-// cap, 1.4 cold); the accepted paths of 64 requests 165 to 185 us (3.7 to 4.1 TB/s of keys).
+// Measured (one B200): 4 x 16384 keys against 8192 rows 465 us (1.34 PFLOP/s at the power
+// cap, 1.5 cold); the accepted paths of 64 requests 147 to 164 us (4.2 to 4.6 TB/s of keys;
+// 178 with the next tile's path looked up only when its turn came).
 // One CTA alone, with two 32 KB stages for the query rows, took 588 and 195 us.  Letting the
 // keys pass through 6, 8, 10 or 11 of the stages instead of keeping them cost 3 to 20% for the
 // accepted paths: fewer bytes of keys on their way, or too few query stages.
@@ -181,13 +182,12 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
   const Pipe pipe{base, abort_flag, p.err};
   auto even = [&](int bar) { return map_to_rank(pipe.bar(bar), (uint32_t)(rank & ~1)); };
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0u;
-    for (int i = 0; i < NBAR; ++i) {
-      const int n = i >= Z_FULL && i < Z_FULL + NS ? 32 : i >= Z_FREE && i < Z_FREE + NS ? 8
-                    : i >= S_FREE && i < S_FREE + NS ? 16 : i >= P_FULL && i < P_FULL + 2 && pairs > 1 ? 128 * (pairs - 1) : 1;
-      mbar_init(base + 8 * i, n);
-    }
+  if (threadIdx.x == 0) *abort_flag = 0u;
+  if (threadIdx.x < NBAR) {                             // a thread each: by one, 1600 cycles
+    const int i = threadIdx.x;
+    const int n = i >= Z_FULL && i < Z_FULL + NS ? 32 : i >= Z_FREE && i < Z_FREE + NS ? 8
+                  : i >= S_FREE && i < S_FREE + NS ? 16 : i >= P_FULL && i < P_FULL + 2 && pairs > 1 ? 128 * (pairs - 1) : 1;
+    mbar_init(base + 8 * i, n);
     fence_mbar_init();
   }
   if (warp == 3) {
@@ -200,15 +200,14 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
     tma_prefetch_desc(&tm_c);
     tma_prefetch_desc(&tm_r);
   }
+  Cursor cur;
+  int bad;
+  cur.start(p, cluster, clusters);
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                       // barriers of all CTAs are ready
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + OFF_TMEM), 0);
-
-  Cursor cur;
-  int bad;
-  if (warp < 4) cur.start(p, cluster, clusters);
 
   if (warp == 0) {
     // ------------------------------------------------------------ K
@@ -250,32 +249,50 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
   } else if (warp == 1) {
     // ------------------------------------------------------------ Q
     uint32_t it = 0;
-    bool ok = true;
-    while (ok && cur.next(p, bad)) {
-      if (bad) continue;
-      for (int t = pr; t < cur.tiles && ok; t += pairs) {
-        const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0), first = half * ((nodes + 1) >> 1);
-        // This CTA's nodes: its half of the columns.  The odd CTA always has one, the last one
-        // again where there is none for it: were a stage filled without it, the even CTA could
-        // go round the stage's barriers once more before the odd one looked at them.
-        const int mine = half ? max(1, nodes >> 1) : (nodes + 1) >> 1, boxes = ((nodes + 1) >> 1) + max(1, nodes >> 1);
-        const int bytes = (p.linear ? 2 * p.linear : boxes * p.H) * 128;
-        // lane i has the box of this CTA's node i (8 at most): first row of the flat [B n H] query
-        const int row = p.linear ? (cur.b * p.n + m0 + first) * p.H
-                                 : (cur.b * p.n + node_at(p, cur.b, m0 + min(first + lane, nodes - 1))) * p.H;
-        const bool issue = p.linear ? lane == 0 : lane < mine;
-        for (int c = 0; c < NCH; ++c, ++it) {
-          const uint32_t st = it % NQ;
-          if (!(ok = pipe.wait_warp(Q_FREE + st, ((it / NQ) & 1u) ^ 1u))) break;
-          const uint32_t bar = even(Q_FULL + st);
-          if (lane == 0 && half == 0) mbar_arrive_expect_tx(pipe.bar(Q_FULL + st), bytes);
-          __syncwarp();
-          if (issue)
-            tma_load_3d_pair(q_at + st * STAGE + lane * p.Hp * 128, c < 8 ? &tm_qa : &tm_qr, c < 8 ? c * 64 : 0, row, 0,
-                             bar);
-          __syncwarp();
-        }
+    // The next tile of this pair, and what its stages take: looked up while the ring is full,
+    // for the path costs a trip to memory.
+    int t = 0, row = 0, bytes = 0;
+    bool issue = false;
+    cur.tiles = 0;
+    auto advance = [&]() -> bool {
+      t += pairs;
+      while (t >= cur.tiles) {
+        if (!cur.next(p, bad)) return false;
+        t = pr;                                         // (a request without work has no tiles)
       }
+      const int m0 = t * p.per_tile, nodes = min(p.per_tile, cur.count - m0), first = half * ((nodes + 1) >> 1);
+      // This CTA's nodes: its half of the columns.  The odd CTA always has one, the last one
+      // again where there is none for it: were a stage filled without it, the even CTA could
+      // go round the stage's barriers once more before the odd one looked at them.
+      const int mine = half ? max(1, nodes >> 1) : (nodes + 1) >> 1, boxes = ((nodes + 1) >> 1) + max(1, nodes >> 1);
+      bytes = (p.linear ? 2 * p.linear : boxes * p.H) * 128;
+      // lane i has the box of this CTA's node i (8 at most): first row of the flat [B n H] query
+      row = p.linear ? (cur.b * p.n + m0 + first) * p.H
+                     : (cur.b * p.n + node_at(p, cur.b, m0 + min(first + lane, nodes - 1))) * p.H;
+      issue = p.linear ? lane == 0 : lane < mine;
+      return true;
+    };
+    int row_now = 0, bytes_now = 0, c = NQ;
+    bool issue_now = false, live = false, more = false;
+    for (;;) {
+      if (c == NQ) more = advance();                    // (first of all, too: no tile is live yet)
+      if (!live || c == NCH) {
+        if (!more) break;
+        row_now = row, bytes_now = bytes, issue_now = issue;
+        live = true;
+        c = 0;
+      }
+      const uint32_t st = it % NQ;
+      if (!pipe.wait_warp(Q_FREE + st, ((it / NQ) & 1u) ^ 1u)) break;
+      const uint32_t bar = even(Q_FULL + st);
+      if (lane == 0 && half == 0) mbar_arrive_expect_tx(pipe.bar(Q_FULL + st), bytes_now);
+      __syncwarp();
+      if (issue_now)
+        tma_load_3d_pair(q_at + st * STAGE + lane * p.Hp * 128, c < 8 ? &tm_qa : &tm_qr, c < 8 ? c * 64 : 0, row_now, 0,
+                         bar);
+      __syncwarp();
+      ++c;
+      ++it;
     }
     if (half == 0)
       for (uint32_t j = it > NQ ? it - NQ : 0; j < it; ++j) pipe.drain(Q_FULL + j % NQ, (j / NQ) & 1u);
@@ -354,7 +371,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t ts = 0, un = 0;
     bool ok = true;
-    cur.start(p, cluster, clusters);
     while (cur.next(p, bad)) {
       if (bad) {
         if (tid == 0 && rank == 0) raise_dev_error(p.err, bad);
@@ -453,9 +469,15 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
           mbar_arrive_remote(map_to_rank(pipe.bar(P_FULL + slot), (uint32_t)half));
         } else {
           if (pairs > 1) {
-            if (!(ok = __all_sync(0xffffffffu, pipe.wait_remote(P_FULL + slot, turn)))) continue;
+            ok = pipe.wait_remote(P_FULL + slot, turn);
             const float* part = reinterpret_cast<const float*>(gbase + OFF_PART) + slot * (MAXP - 1) * BK;
             for (int i = 0; i < pairs - 1; ++i) sum += part[i * BK + r];
+            if (named_bar_red_or(2, 128, !ok)) {        // everyone has read the parts, or gives up
+              ok = false;
+              continue;
+            }
+            // (before the weights are stored: the arrival would wait for that)
+            if (r < pairs - 1) mbar_arrive_remote(map_to_rank(pipe.bar(P_FREE + slot), (uint32_t)(2 * (r + 1) + half)));
           }
           if (!out) {
             float* wo = p.w_out + (int64_t)cur.b * p.wo;
@@ -466,10 +488,6 @@ weights_kernel(const __grid_constant__ CUtensorMap tm_qa, const __grid_constant_
                 for (int m = 0; m < cur.count; ++m)
                   if (p.path[(size_t)cur.b * p.n + m] == k) wo[cur.L + m] = sum;
             }
-          }
-          if (pairs > 1) {
-            named_bar_sync(2, 128);                     // everyone has read the parts
-            if (r < pairs - 1) mbar_arrive_remote(map_to_rank(pipe.bar(P_FREE + slot), (uint32_t)(2 * (r + 1) + half)));
           }
         }
       }
