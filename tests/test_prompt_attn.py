@@ -156,6 +156,26 @@ def test_groups_and_expanded_heads(kd, H, Hk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,klens,H,Hk,rope,heads", [
+    ([65, 3, 0, 200], None, 32, 2, True, (0, 15, 16, 31)), ([1, 9, 16, 17], None, 16, 2, False, None),
+    ([33, 1, 130], [40, 500, 131], 32, 4, True, (0, 7, 8, 31)), ([300, 2], None, 64, 1, False, (0, 33, 63)),
+    ([1] * 70, [77] * 70, 8, 2, False, (0, 3, 4)), ([5, 70, 4], [3, 0, 9], 8, 1, False, None),
+    ([2300, 2100], None, 8, 1, False, (0, 7)), ([2049], [2100], 4, 2, True, (1, 2)), ([2050], None, 6, 2, False, (0, 4))])
+def test_heads_that_share_keys(kd, lens, klens, H, Hk, rope, heads):
+    """Groups of 2 to 64 heads that share a tile (short prompts) and groups that do not (long ones,
+    groups of three); what lies behind the last sequence stays."""
+    klens = klens or lens
+    T = sum(lens)
+    q, k, v, kr, full = inputs(lens + [3], klens, H, Hk, rope, seed=T)
+    out = torch.full((T + 3, H, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 3, H), 4.0, device="cuda")
+    kd.kd_prompt_attn(q[..., :128], k, v, cu_of(lens), q_rope=q[..., 128:] if rope else None, k_rope=kr,
+                      cu_seqlens_k=cu_of(klens), scale=0.07, out=out, lse=lse)
+    check(out, lse, q, full, v, lens, klens, 0.07, heads=heads)
+    assert bool((out[T:] == 3.0).all()) and bool((lse[T:] == 4.0).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("big", [8.0, 40.0])
 def test_peaked_scores(kd, big):
     """Scores that climb along the keys: the running maximum moves in every tile."""

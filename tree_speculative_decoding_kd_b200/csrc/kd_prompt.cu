@@ -3,7 +3,8 @@
 //   s_ij = scale (q_i . k_j), j <= i + nk - nq;  out_i = softmax(s_i) . v;  lse_i = ln sum exp s_ij
 //
 // A unit is (sequence, 256 query rows, head): two 128-row tiles that share every key and
-// value tile of 128 keys.  Each tile has its own score tile S (128 TMEM columns) and output
+// value tile of 128 keys.  PACK: the rows are 256 >> shift tokens, each with the 1 << shift heads
+// of one key head.  Each tile has its own score tile S (128 TMEM columns) and output
 // O (128 columns), 512 columns in all, and its own four softmax warps (a thread per row), so
 // that one tile's products run while the other's exponentials do.
 //
@@ -91,14 +92,16 @@ struct Params {
   uint16_t* out;
   float* lse;
   int32_t* err;
-  int B, T, Tk, H, group, slots;
+  int B, T, Tk, H, slots;
+  int shift;                          // a tile's rows are 128 >> shift tokens of 1 << shift heads each
+  int heads, group;                   // units beside each other (H >> shift), of which `group` share a key head
   int k_heads, r_heads, v_heads;      // 0: one head for all (head coordinate 0)
   float scale, scale_log2;
 };
 
 // What a unit is; n[i]: key tiles of query tile i.
 struct Unit {
-  int q0, nq, k0, nk, row, head;      // row: first query row of the unit inside its sequence
+  int q0, nq, k0, nk, row, head;      // row: first token of the unit inside its sequence; head: among p.heads
   int n0, n1;
   __device__ __forceinline__ int tiles(int i) const { return i ? n1 : n0; }
 };
@@ -107,10 +110,10 @@ struct Unit {
 template <int N>
 __device__ __forceinline__ uint32_t wrap(uint32_t x) { return x >= N ? x - N : x; }
 
-// Key tiles that the 128 rows from `row` on see.
-__device__ __forceinline__ int tiles_of(int nq, int nk, int row) {
+// Key tiles that the `rows` tokens from `row` on see.
+__device__ __forceinline__ int tiles_of(int nq, int nk, int row, int rows) {
   if (row >= nq) return 0;
-  const int last = min(row + BM, nq) - 1;
+  const int last = min(row + rows, nq) - 1;
   const int keys = min((int64_t)nk, (int64_t)last + nk - nq + 1);
   return keys > 0 ? (keys + BN - 1) / BN : 0;
 }
@@ -186,13 +189,14 @@ __device__ __forceinline__ int cancelled_block(uint32_t src) {
   return ok ? (int)x : -1;
 }
 
-template <bool ROPE>
+template <bool ROPE, bool PACK>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
               const __grid_constant__ CUtensorMap tm_v, const Params p) {
   constexpr int KC = ROPE ? 3 : 2;            // 64-column chunks of a key
   constexpr int RING = ROPE ? 8 : 10;
+  const int shift = PACK ? p.shift : 0;
   extern __shared__ uint8_t dyn[];
   uint8_t* gbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
   const uint32_t base = smem_u32(gbase);
@@ -250,12 +254,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     int u = (int)blockIdx.x, k = 0, asks = 0;
     bool ok = true;
     while (true) {
-      // unit u: slot (256 rows) and head; sequence b has the slots from cu[b] / 256 + b on
-      const int slot = p.slots - 1 - u / p.H, head = u % p.H;
+      // unit u: slot (256 rows, 1 << bits tokens) and head; sequence b has the slots from
+      // (cu[b] >> bits) + b on
+      const int slot = p.slots - 1 - u / p.heads, head = u % p.heads, bits = 8 - shift;
       int lo = 0, hi = p.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.cu_q[mid] / (2 * BM) + mid <= slot) lo = mid;
+        if ((p.cu_q[mid] >> bits) + mid <= slot) lo = mid;
         else hi = mid - 1;
       }
       Unit w;
@@ -263,14 +268,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       w.nq = p.cu_q[lo + 1] - w.q0;
       w.k0 = p.cu_k ? p.cu_k[lo] : w.q0;
       w.nk = p.cu_k ? p.cu_k[lo + 1] - w.k0 : w.nq;
-      const int64_t row = (int64_t)(slot - w.q0 / (2 * BM) - lo) * (2 * BM);
+      const int64_t row = (int64_t)(slot - (w.q0 >> bits) - lo) << bits;
       if (row >= 0 && row < w.nq) {
         w.row = (int)row;
         if (!(ok = pipe.wait_warp(U_FREE + k % NS, ((k / NS) & 1) ^ 1))) break;
         if (lane == 0) {
           int4* s = reinterpret_cast<int4*>(gbase + OFF_UNIT + (k % NS) * 32);
           s[0] = make_int4(w.q0, w.nq, w.k0, w.nk);
-          s[1] = make_int4(w.row, head, tiles_of(w.nq, w.nk, w.row), tiles_of(w.nq, w.nk, w.row + BM));
+          const int rows = BM >> shift;
+          s[1] = make_int4(w.row, head, tiles_of(w.nq, w.nk, w.row, rows), tiles_of(w.nq, w.nk, w.row + rows, rows));
           mbar_arrive(pipe.bar(U_FULL + k % NS));
         }
         __syncwarp();
@@ -334,11 +340,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!pipe.wait_warp(Q_FREE + i, (nq[i] & 1u) ^ 1u)) return false;
         if (lane == 0) {
           const uint32_t bar = pipe.bar(Q_FULL + i), dst = q_smem + i * KC * CHUNK;
-          const int row = u.q0 + u.row + i * BM;
+          const int row = u.q0 + u.row + i * (BM >> shift), head = u.head << shift;
           mbar_arrive_expect_tx(bar, KC * CHUNK);
-          tma_load_3d(dst, &tm_q, 0, u.head, row, bar);
-          tma_load_3d(dst + CHUNK, &tm_q, 64, u.head, row, bar);
-          if (ROPE) tma_load_3d(dst + 2 * CHUNK, &tm_qr, 0, u.head, row, bar);
+          tma_load_3d(dst, &tm_q, 0, head, row, bar);
+          tma_load_3d(dst + CHUNK, &tm_q, 64, head, row, bar);
+          if (ROPE) tma_load_3d(dst + 2 * CHUNK, &tm_qr, 0, head, row, bar);
         }
         __syncwarp();
         ++nq[i];
@@ -515,7 +521,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
-      const int n = u.tiles(i), row = u.row + i * BM + r;
+      const int n = u.tiles(i), row = u.row + ((i * BM + r) >> shift);
       // keys this row sees, and the first and the last row of the warp
       const int64_t off = (int64_t)u.nk - u.nq + 1;
       const int lim = (int)max((int64_t)0, min((int64_t)u.nk, row + off));
@@ -608,7 +614,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       }
       if (!ok) break;
       const bool mine = row < u.nq;
-      const int64_t at = ((int64_t)(u.q0 + row) * p.H + u.head);
+      const int64_t at = (int64_t)(u.q0 + row) * p.H + (u.head << shift) + (r & ((1 << shift) - 1));
       if (n > 0) {
         if (!(ok = pipe.wait_warp(O_DONE + i, nu & 1u))) break;
         ++nu;
@@ -668,8 +674,18 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
       (Tk && (!view_ok(k_nope, knt, knh, Tk) || !view_ok(v, vt, vh, Tk))) ||
       (q_rope && (!view_ok(q_rope, qrt, qrh, T) || (H > 1 && qrh == 0) || (Tk && !view_ok(k_rope, krt, krh, Tk)))))
     return KD_EINVAL;
-  const int64_t slots = T / (2 * pr::BM) + (int64_t)B;
-  if (slots * H > INT32_MAX) return KD_EINVAL;
+  // Short prompts' heads that share a key head fill a tile together, where their number is a
+  // power of two: 32 prompts of 1 to 300 tokens, 32 heads on 4, 36 us against 45 with a head a
+  // tile, 8 of 1000 to 2000 184 against 196, 27 of one or two tokens over 340 keys (32 on 8) 20
+  // against 45.  Long ones leave few rows empty, and a tile's rows in one piece are faster: 4 of
+  // 4096 tokens, 16 heads on 2, 283 against 291, one of 16384 1016 against 1028.
+  int shift = 0;
+  const int group = H / Hk;
+  if ((group & (group - 1)) == 0 && T < (int64_t)2048 * B)
+    while (1 << shift < group) ++shift;
+  const int heads = H >> shift;
+  const int64_t slots = (T >> (8 - shift)) + (int64_t)B;
+  if (slots * heads > INT32_MAX) return KD_EINVAL;
   int st = device_sms(nullptr);
   if (st) return st;
   int dev = 0;
@@ -677,37 +693,37 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
   static std::once_flag once[64];
   static std::atomic<int> attr[64];
   std::call_once(once[dev], [&] {
-    int s = cuda_status(cudaFuncSetAttribute(pr::prompt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             pr::SMEM),
+    int s = 0;
+    for (const auto kernel : {pr::prompt_kernel<false, false>, pr::prompt_kernel<false, true>,
+                              pr::prompt_kernel<true, false>, pr::prompt_kernel<true, true>})
+      if (!s)
+        s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pr::SMEM),
                         "cudaFuncSetAttribute(prompt_kernel)");
-    if (!s)
-      s = cuda_status(cudaFuncSetAttribute(pr::prompt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           pr::SMEM),
-                      "cudaFuncSetAttribute(prompt_kernel)");
     attr[dev].store(s);
   });
   if ((st = attr[dev].load())) return st;
 
-  pr::Params p{cu_q, cu_k, out, lse, dev_error, B, T, Tk, H, H / Hk, (int)slots, knh > 0, krh > 0, vh > 0,
+  pr::Params p{cu_q, cu_k, out, lse, dev_error, B, T, Tk, H, (int)slots, shift, heads, heads / Hk, knh > 0, krh > 0, vh > 0,
                scale, scale * 1.4426950408889634f};
   const bool rope = q_rope != nullptr;
   CUtensorMap tq, tqr, tk, tkr, tv;
   // without keys the key and value maps are never used: any memory will do
   const kd_bf16_t *kp = Tk ? k_nope : q_nope, *vp = Tk ? v : q_nope, *rp = Tk ? k_rope : q_rope;
-  if ((st = make_tmap3(&tq, q_nope, 128, H, T, qnh, qnt, 1, pr::BM)) ||
+  if ((st = make_tmap3(&tq, q_nope, 128, H, T, qnh, qnt, 1 << shift, pr::BM >> shift)) ||
       (st = make_tmap3(&tk, kp, 128, knh ? Hk : 1, Tk, knh, knt, 1, pr::BN)) ||
       (st = make_tmap3(&tv, vp, 128, vh ? Hk : 1, Tk, vh, vt, 1, 64)))
     return st;
   if (rope) {
-    if ((st = make_tmap3(&tqr, q_rope, 64, H, T, qrh, qrt, 1, pr::BM)) ||
+    if ((st = make_tmap3(&tqr, q_rope, 64, H, T, qrh, qrt, 1 << shift, pr::BM >> shift)) ||
         (st = make_tmap3(&tkr, rp, 64, krh ? Hk : 1, Tk, krh, krt, 1, pr::BN)))
       return st;
   } else {
     tqr = tq;
     tkr = tk;
   }
-  const unsigned grid = (unsigned)(slots * H);
-  if (rope) pr::prompt_kernel<true><<<grid, pr::THREADS, pr::SMEM, stream>>>(tq, tqr, tk, tkr, tv, p);
-  else pr::prompt_kernel<false><<<grid, pr::THREADS, pr::SMEM, stream>>>(tq, tqr, tk, tkr, tv, p);
+  const unsigned grid = (unsigned)(slots * heads);
+  const auto kernel = shift ? (rope ? pr::prompt_kernel<true, true> : pr::prompt_kernel<false, true>)
+                            : (rope ? pr::prompt_kernel<true, false> : pr::prompt_kernel<false, false>);
+  kernel<<<grid, pr::THREADS, pr::SMEM, stream>>>(tq, tqr, tk, tkr, tv, p);
   return launch_status("prompt_kernel");
 }
