@@ -160,10 +160,13 @@ def test_groups_and_expanded_heads(kd, H, Hk):
     ([65, 3, 0, 200], None, 32, 2, True, (0, 15, 16, 31)), ([1, 9, 16, 17], None, 16, 2, False, None),
     ([33, 1, 130], [40, 500, 131], 32, 4, True, (0, 7, 8, 31)), ([300, 2], None, 64, 1, False, (0, 33, 63)),
     ([1] * 70, [77] * 70, 8, 2, False, (0, 3, 4)), ([5, 70, 4], [3, 0, 9], 8, 1, False, None),
-    ([2300, 2100], None, 8, 1, False, (0, 7)), ([2049], [2100], 4, 2, True, (1, 2)), ([2050], None, 6, 2, False, (0, 4))])
+    ([37, 0, 18, 19, 300], None, 14, 2, True, (0, 6, 7, 13)), ([130, 1], [7, 200], 15, 3, False, (0, 4, 5)),
+    ([25, 26, 60], None, 57, 3, False, (0, 18, 19, 56)), ([70, 3], None, 43, 1, False, (0, 42)),
+    ([129], [300], 66, 2, True, (0, 32, 33)), ([2300, 2100], None, 8, 1, False, (0, 7)), ([2049], [2100], 4, 2, True, (1, 2)), ([2050], None, 6, 2, False, (0, 4))])
 def test_heads_that_share_keys(kd, lens, klens, H, Hk, rope, heads):
-    """Groups of 2 to 64 heads that share a tile (short prompts) and groups that do not (long ones,
-    groups of three); what lies behind the last sequence stays."""
+    """Groups of 2 to 64 heads that share a tile (short prompts, with rows to spare or not) and groups
+    that do not (long ones, those that would leave much of it empty); what lies behind the last
+    sequence stays."""
     klens = klens or lens
     T = sum(lens)
     q, k, v, kr, full = inputs(lens + [3], klens, H, Hk, rope, seed=T)

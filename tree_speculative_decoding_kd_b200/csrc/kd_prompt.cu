@@ -3,7 +3,7 @@
 //   s_ij = scale (q_i . k_j), j <= i + nk - nq;  out_i = softmax(s_i) . v;  lse_i = ln sum exp s_ij
 //
 // A unit is (sequence, 256 query rows, head): two 128-row tiles that share every key and
-// value tile of 128 keys.  PACK: the rows are 256 >> shift tokens, each with the 1 << shift heads
+// value tile of 128 keys.  PACK: a tile's rows are 128 / G tokens, each with the G heads
 // of one key head.  Each tile has its own score tile S (128 TMEM columns) and output
 // O (128 columns), 512 columns in all, and its own four softmax warps (a thread per row), so
 // that one tile's products run while the other's exponentials do.
@@ -93,8 +93,8 @@ struct Params {
   float* lse;
   int32_t* err;
   int B, T, Tk, H, slots;
-  int shift;                          // a tile's rows are 128 >> shift tokens of 1 << shift heads each
-  int heads, group;                   // units beside each other (H >> shift), of which `group` share a key head
+  int packed, tokens;                 // a tile's rows are `tokens` (128 / packed) tokens of `packed` heads each
+  int heads, group;                   // units beside each other (H / packed), of which `group` share a key head
   int k_heads, r_heads, v_heads;      // 0: one head for all (head coordinate 0)
   float scale, scale_log2;
 };
@@ -196,7 +196,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_v, const Params p) {
   constexpr int KC = ROPE ? 3 : 2;            // 64-column chunks of a key
   constexpr int RING = ROPE ? 8 : 10;
-  const int shift = PACK ? p.shift : 0;
+  const int packed = PACK ? p.packed : 1, tokens = PACK ? p.tokens : BM;
   extern __shared__ uint8_t dyn[];
   uint8_t* gbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
   const uint32_t base = smem_u32(gbase);
@@ -254,13 +254,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     int u = (int)blockIdx.x, k = 0, asks = 0;
     bool ok = true;
     while (true) {
-      // unit u: slot (256 rows, 1 << bits tokens) and head; sequence b has the slots from
-      // (cu[b] >> bits) + b on
-      const int slot = p.slots - 1 - u / p.heads, head = u % p.heads, bits = 8 - shift;
+      // unit u: slot (two tiles' tokens) and head; sequence b has the slots from
+      // cu[b] / (2 tokens) + b on
+      const int slot = p.slots - 1 - u / p.heads, head = u % p.heads;
       int lo = 0, hi = p.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((p.cu_q[mid] >> bits) + mid <= slot) lo = mid;
+        if (p.cu_q[mid] / (2 * tokens) + mid <= slot) lo = mid;
         else hi = mid - 1;
       }
       Unit w;
@@ -268,15 +268,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       w.nq = p.cu_q[lo + 1] - w.q0;
       w.k0 = p.cu_k ? p.cu_k[lo] : w.q0;
       w.nk = p.cu_k ? p.cu_k[lo + 1] - w.k0 : w.nq;
-      const int64_t row = (int64_t)(slot - (w.q0 >> bits) - lo) << bits;
+      const int64_t row = (int64_t)(slot - w.q0 / (2 * tokens) - lo) * (2 * tokens);
       if (row >= 0 && row < w.nq) {
         w.row = (int)row;
         if (!(ok = pipe.wait_warp(U_FREE + k % NS, ((k / NS) & 1) ^ 1))) break;
         if (lane == 0) {
           int4* s = reinterpret_cast<int4*>(gbase + OFF_UNIT + (k % NS) * 32);
           s[0] = make_int4(w.q0, w.nq, w.k0, w.nk);
-          const int rows = BM >> shift;
-          s[1] = make_int4(w.row, head, tiles_of(w.nq, w.nk, w.row, rows), tiles_of(w.nq, w.nk, w.row + rows, rows));
+          s[1] = make_int4(w.row, head, tiles_of(w.nq, w.nk, w.row, tokens),
+                           tiles_of(w.nq, w.nk, w.row + tokens, tokens));
           mbar_arrive(pipe.bar(U_FULL + k % NS));
         }
         __syncwarp();
@@ -340,8 +340,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!pipe.wait_warp(Q_FREE + i, (nq[i] & 1u) ^ 1u)) return false;
         if (lane == 0) {
           const uint32_t bar = pipe.bar(Q_FULL + i), dst = q_smem + i * KC * CHUNK;
-          const int row = u.q0 + u.row + i * (BM >> shift), head = u.head << shift;
-          mbar_arrive_expect_tx(bar, KC * CHUNK);
+          const int row = u.q0 + u.row + i * tokens, head = u.head * packed;
+          mbar_arrive_expect_tx(bar, PACK ? KC * tokens * packed * 128 : KC * CHUNK);
           tma_load_3d(dst, &tm_q, 0, head, row, bar);
           tma_load_3d(dst + CHUNK, &tm_q, 64, head, row, bar);
           if (ROPE) tma_load_3d(dst + 2 * CHUNK, &tm_qr, 0, head, row, bar);
@@ -511,6 +511,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax and output of one tile
     const int i = warp >> 2, r = threadIdx.x & 127;
+    const int r_token = PACK ? r / packed : r, r_head = PACK ? r - r_token * packed : 0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = t_s + i * BN + lanes, o_at = t_o + i * BN + lanes;
     uint32_t ns = 0, nu = 0;                            // key tiles, units with work
@@ -521,7 +522,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(pipe.bar(U_FREE + k % NS));
       if (u.q0 < 0) break;
-      const int n = u.tiles(i), row = u.row + ((i * BM + r) >> shift);
+      const int n = u.tiles(i), row = u.row + i * tokens + r_token;
       // keys this row sees, and the first and the last row of the warp
       const int64_t off = (int64_t)u.nk - u.nq + 1;
       const int lim = (int)max((int64_t)0, min((int64_t)u.nk, row + off));
@@ -613,8 +614,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         l += l0 + l1;
       }
       if (!ok) break;
-      const bool mine = row < u.nq;
-      const int64_t at = (int64_t)(u.q0 + row) * p.H + (u.head << shift) + (r & ((1 << shift) - 1));
+      const bool mine = row < u.nq && (!PACK || r_token < tokens);      // (128 rows are not all used)
+      const int64_t at = (int64_t)(u.q0 + row) * p.H + u.head * packed + r_head;
       if (n > 0) {
         if (!(ok = pipe.wait_warp(O_DONE + i, nu & 1u))) break;
         ++nu;
@@ -674,17 +675,16 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
       (Tk && (!view_ok(k_nope, knt, knh, Tk) || !view_ok(v, vt, vh, Tk))) ||
       (q_rope && (!view_ok(q_rope, qrt, qrh, T) || (H > 1 && qrh == 0) || (Tk && !view_ok(k_rope, krt, krh, Tk)))))
     return KD_EINVAL;
-  // Short prompts' heads that share a key head fill a tile together, where their number is a
-  // power of two: 32 prompts of 1 to 300 tokens, 32 heads on 4, 36 us against 45 with a head a
-  // tile, 8 of 1000 to 2000 184 against 196, 27 of one or two tokens over 340 keys (32 on 8) 20
-  // against 45.  Long ones leave few rows empty, and a tile's rows in one piece are faster: 4 of
-  // 4096 tokens, 16 heads on 2, 283 against 291, one of 16384 1016 against 1028.
-  int shift = 0;
-  const int group = H / Hk;
-  if ((group & (group - 1)) == 0 && T < (int64_t)2048 * B)
-    while (1 << shift < group) ++shift;
-  const int heads = H >> shift;
-  const int64_t slots = (T >> (8 - shift)) + (int64_t)B;
+  // Short prompts' heads that share a key head fill a tile together.  With a head a tile and so:
+  // 32 prompts of 1 to 300 tokens, 28 heads on 4, 40 and 32 us; 8 of 1000 to 2000, 32 on 4, 193 and
+  // 179; 27 of one or two tokens over 340 keys, 32 on 8, 45 and 20; but 4 of just 1024, 40 on 8,
+  // 66 and 68.  Long ones leave few rows empty, and a tile's rows in one piece are faster: 4 of
+  // 4096 tokens, 16 heads on 2, 283 and 291, one of 16384 1016 and 1028.  Nor do groups share a
+  // tile that would leave an eighth of it empty (22 or more heads as a rule).
+  const int group = H / Hk, full = pr::BM / group * group;
+  const int packed = T < (int64_t)2048 * B && full >= pr::BM * 7 / 8 ? group : 1;
+  const int tokens = pr::BM / packed, heads = H / packed;
+  const int64_t slots = T / (2 * tokens) + (int64_t)B;
   if (slots * heads > INT32_MAX) return KD_EINVAL;
   int st = device_sms(nullptr);
   if (st) return st;
@@ -703,18 +703,18 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
   });
   if ((st = attr[dev].load())) return st;
 
-  pr::Params p{cu_q, cu_k, out, lse, dev_error, B, T, Tk, H, (int)slots, shift, heads, heads / Hk, knh > 0, krh > 0, vh > 0,
+  pr::Params p{cu_q, cu_k, out, lse, dev_error, B, T, Tk, H, (int)slots, packed, tokens, heads, heads / Hk, knh > 0, krh > 0, vh > 0,
                scale, scale * 1.4426950408889634f};
   const bool rope = q_rope != nullptr;
   CUtensorMap tq, tqr, tk, tkr, tv;
   // without keys the key and value maps are never used: any memory will do
   const kd_bf16_t *kp = Tk ? k_nope : q_nope, *vp = Tk ? v : q_nope, *rp = Tk ? k_rope : q_rope;
-  if ((st = make_tmap3(&tq, q_nope, 128, H, T, qnh, qnt, 1 << shift, pr::BM >> shift)) ||
+  if ((st = make_tmap3(&tq, q_nope, 128, H, T, qnh, qnt, packed, tokens)) ||
       (st = make_tmap3(&tk, kp, 128, knh ? Hk : 1, Tk, knh, knt, 1, pr::BN)) ||
       (st = make_tmap3(&tv, vp, 128, vh ? Hk : 1, Tk, vh, vt, 1, 64)))
     return st;
   if (rope) {
-    if ((st = make_tmap3(&tqr, q_rope, 64, H, T, qrh, qrt, 1 << shift, pr::BM >> shift)) ||
+    if ((st = make_tmap3(&tqr, q_rope, 64, H, T, qrh, qrt, packed, tokens)) ||
         (st = make_tmap3(&tkr, rp, 64, krh ? Hk : 1, Tk, krh, krt, 1, pr::BN)))
       return st;
   } else {
@@ -722,7 +722,7 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
     tkr = tk;
   }
   const unsigned grid = (unsigned)(slots * heads);
-  const auto kernel = shift ? (rope ? pr::prompt_kernel<true, true> : pr::prompt_kernel<false, true>)
+  const auto kernel = packed > 1 ? (rope ? pr::prompt_kernel<true, true> : pr::prompt_kernel<false, true>)
                             : (rope ? pr::prompt_kernel<true, false> : pr::prompt_kernel<false, false>);
   kernel<<<grid, pr::THREADS, pr::SMEM, stream>>>(tq, tqr, tk, tkr, tv, p);
   return launch_status("prompt_kernel");
