@@ -372,6 +372,27 @@ def test_evict_many_requests_and_long(kd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["equal", "random", "ties"])
+def test_evict_longer_than_a_cluster_reads_at_once(kd, kind):
+    """Caches numbered in several steps (a cluster holds 32768 slots), with equal weights on both
+    sides of a step, into another cache; unaligned rows of weights."""
+    Ls, keep, sink, recent = [70001, 33000, 32769], 21000, 3, 700
+    B, cap = len(Ls), max(Ls)
+    c, r = normal(B, cap, 512, seed=1), normal(B, cap, 64, seed=2)
+    rng = np.random.default_rng(5)
+    w = torch.from_numpy(np.stack([WEIGHTS[kind](rng, cap) for _ in range(B)]))
+    win = torch.empty(B, cap + 3, device="cuda")[:, :cap]
+    win.copy_(w)
+    dst = torch.zeros(B, keep, 512, dtype=torch.bfloat16, device="cuda"), \
+        torch.zeros(B, keep, 64, dtype=torch.bfloat16, device="cuda")
+    lens = i32(Ls)
+    kept, wo, lo = kd.kd_kv_evict(c, r, lens, win, keep, sink, recent, c_dst=dst[0], r_dst=dst[1])
+    src, now = [x.view(torch.int16) for x in (c, r)], [x.view(torch.int16) for x in dst]
+    check_evict(kept.cpu(), wo, lo.cpu(), Ls, w, keep, sink, recent, lambda b, s: [x[b, s] for x in src],
+                lambda b, s: [x[b, s] for x in now], None)
+
+
+@pytest.mark.gpu
 def test_weights_of_a_repeated_path_entry(kd):
     """A path that names a node twice counts its rows twice and writes its slot's weight at both places."""
     n, H, L, cap = 5, 16, 200, 230

@@ -270,6 +270,21 @@ def test_strides_repeat_streams_and_graph(kd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk", [(8, 2), (7, 1), (3, 3)])
+def test_heads_before_tokens(kd, H, Hk):
+    """Inputs laid out [heads][tokens][elements], each head's tokens in a row, and keys of which
+    only every second token is used."""
+    lens = [19, 1, 140]
+    T = sum(lens)
+    q = normal(H, T, 192, seed=1).transpose(0, 1)
+    k = normal(Hk, 2 * T, 128, seed=2).transpose(0, 1)[::2]
+    kr = normal(1, T, 64, seed=3).transpose(0, 1)[:, 0]
+    v = normal(Hk, T, 136, seed=4).transpose(0, 1)[..., 8:]
+    out, lse = kd.kd_prompt_attn(q[..., :128], k, v, cu_of(lens), q_rope=q[..., 128:], k_rope=kr, scale=0.06)
+    check(out, lse, q, torch.cat([k, kr[:, None].expand(-1, Hk, -1)], -1), v, lens, lens, 0.06)
+
+
+@pytest.mark.gpu
 def test_long_prompt_sampled_heads(kd):
     lens = [5000]
     q, k, v, kr, full = inputs(lens, lens, 16, 2, True, seed=7)
