@@ -393,6 +393,35 @@ def test_evict_longer_than_a_cluster_reads_at_once(kd, kind):
 
 
 @pytest.mark.gpu
+def test_results_belong_to_the_stream_of_the_call(kd):
+    """A call on another stream than the current one, which is busy: what the call allocates (zeros
+    behind the stored weights) is not filled by the current stream after the kernels ran."""
+    B, cap, n, H, keep = 2, 300, 3, 16, 100
+    c, r = normal(B, cap, 512, seed=1), normal(B, cap, 64, seed=2)
+    qa, qr = normal(B, n, H, 512, seed=3), normal(B, n, H, 64, seed=4)
+    vis, _ = kd.kd_tree_build_mask(i32([[-1, 0, 1]] * B))
+    lens, lse = i32([250, 297]), torch.zeros(B, n, H, device="cuda")
+    dst = torch.empty(B, keep, 512, dtype=torch.bfloat16, device="cuda"), \
+        torch.empty(B, keep, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.rand(B, cap, device="cuda")
+
+    def both(stream):
+        ww = kd.kd_kv_attn_weights(qa, qr, c, r, lens, vis, lse, scale=0.01, stream=stream)
+        kept, wo, lo = kd.kd_kv_evict(c, r, lens, w, keep, 2, 10, c_dst=dst[0], r_dst=dst[1], stream=stream)
+        return ww, kept, wo, lo
+
+    want = both(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)                      # the current stream is busy for about 0.1 s
+    got = both(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y) and bool((x != 0).any())
+
+
+@pytest.mark.gpu
 def test_weights_of_a_repeated_path_entry(kd):
     """A path that names a node twice counts its rows twice and writes its slot's weight at both places."""
     n, H, L, cap = 5, 16, 200, 230

@@ -437,6 +437,14 @@ def _on_device(*tensors) -> int:
     return dev
 
 
+def _new(stream, make, *shape, dtype, device):
+    """A result tensor by make (torch.empty, torch.zeros), allocated and filled on the call's stream."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _typed(t, dtype, name, shape=None):
     """Contiguous tensor of `dtype` and, when given, of `shape`."""
     if t.dtype is not dtype or not t.is_contiguous():
@@ -513,7 +521,7 @@ def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, e
     if q_weight is not None:
         _typed(q_weight, torch.bfloat16, "q_weight", (D,))
     if q_out is None:
-        q_out = torch.empty(T, H, D, dtype=torch.bfloat16, device=q.device)
+        q_out = _new(stream, torch.empty, T, H, D, dtype=torch.bfloat16, device=q.device)
     _, _, _, qot, qoh = _heads(q_out, "q_out", T, H, D)
     Hk = kt = kh = kot = koh = 0
     if k is not None:
@@ -521,7 +529,7 @@ def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, e
         if k_weight is not None:
             _typed(k_weight, torch.bfloat16, "k_weight", (D,))
         if k_out is None:
-            k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=q.device)
+            k_out = _new(stream, torch.empty, T, Hk, D, dtype=torch.bfloat16, device=q.device)
         _, _, _, kot, koh = _heads(k_out, "k_out", T, Hk, D)
     _call_qk_norm_rope(q.data_ptr(), qt, qh, _addr(k), kt, kh, _addr(q_weight), _addr(k_weight), eps,
         rope_table.data_ptr(), max_pos, positions.data_ptr(), T, H, Hk, D, rot, rot_offset, interleaved,
@@ -529,7 +537,7 @@ def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, e
     return q_out, k_out
 
 
-def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B, q_rope_in, q_rope_out):
+def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B, q_rope_in, q_rope_out, stream):
     _typed(cache_lens, torch.int32, "cache_lens")
     if B is None:
         B = cache_lens.shape[0]
@@ -551,7 +559,7 @@ def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
     if q_rope_in is not None:
         _, H, _, qt, qh = _heads(q_rope_in, "q_rope_in", T, None, D_R)
         if q_rope_out is None:
-            q_rope_out = torch.empty(T, H, D_R, dtype=torch.bfloat16, device=kv.device)
+            q_rope_out = _new(stream, torch.empty, T, H, D_R, dtype=torch.bfloat16, device=kv.device)
         _typed(q_rope_out, torch.bfloat16, "q_rope_out", (T, H, D_R))
     elif q_rope_out is not None:
         raise ValueError("q_rope_out without q_rope_in")
@@ -569,7 +577,7 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
                dev_error)
     rows, sc, sr, cap = _cache(c_kv, k_rope)
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
-                                                       q_rope_in, q_rope_out)
+                                                       q_rope_in, q_rope_out, stream)
     if rows != B:
         raise ValueError("the cache must hold B requests")
     _call_kv_norm_rope_write(c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap, cache_lens.data_ptr(), kv.data_ptr(),
@@ -586,7 +594,7 @@ def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_l
     dev = _on_device(c_pages, r_pages, page_table, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in,
                q_rope_out, dev_error)
     B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
-                                                       q_rope_in, q_rope_out)
+                                                       q_rope_in, q_rope_out, stream)
     sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, B)
     _call_kv_norm_rope_write_paged(c_pages.data_ptr(), r_pages.data_ptr(), sc, sr, int(page_size),
         page_table.data_ptr(), M, N, cache_lens.data_ptr(), kv.data_ptr(), kv.stride(0), _addr(kv_weight), eps,
@@ -625,9 +633,9 @@ def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu
     if scale is None:
         scale = 1.0 / math.sqrt(128.0 if q_rope is None else 192.0)
     if out is None:
-        out = torch.empty(T, H, 128, dtype=torch.bfloat16, device=q_nope.device)
+        out = _new(stream, torch.empty, T, H, 128, dtype=torch.bfloat16, device=q_nope.device)
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=q_nope.device)
+        lse = _new(stream, torch.empty, T, H, dtype=torch.float32, device=q_nope.device)
     _typed(out, torch.bfloat16, "out", (T, H, 128))
     _typed(lse, torch.float32, "lse", (T, H))
     _call_prompt_attn(q_nope.data_ptr(), qnt, qnh, _addr(q_rope), qrt, qrh, k_nope.data_ptr(), knt, knh,
@@ -642,7 +650,7 @@ def _weight_rows(w, B, cap, name):
     return w.stride(0) if B > 1 else max(w.stride(0), w.shape[1])
 
 
-def _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, cap):
+def _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, cap, stream):
     _typed(q_abs, torch.bfloat16, "q_abs")
     if q_abs.dim() != 4 or q_abs.shape[3] != D_C:
         raise ValueError("q_abs must be [B][n][H][512]")
@@ -659,7 +667,7 @@ def _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
         _typed(path, torch.int32, "path", (B, n))
         _typed(length, torch.int32, "length", (B,))
     if weights_out is None:
-        weights_out = torch.zeros(B, cap, dtype=torch.float32, device=q_abs.device)
+        weights_out = _new(stream, torch.zeros, B, cap, dtype=torch.float32, device=q_abs.device)
     wi = _weight_rows(weights_in, B, cap, "weights_in") if weights_in is not None else 0
     return B, n, H, wi, _weight_rows(weights_out, B, cap, "weights_out"), weights_out
 
@@ -673,7 +681,7 @@ def kd_kv_attn_weights(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path=N
     dev = _on_device(q_abs, q_rope, c_kv, k_rope, cache_lens, vis, lse, path, length, weights_in, weights_out, dev_error)
     rows, sc, sr, cap = _cache(c_kv, k_rope)
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
-                                                 weights_out, cap)
+                                                 weights_out, cap, stream)
     if rows != B:
         raise ValueError("the cache must hold B requests")
     _call_kv_attn_weights(q_abs.data_ptr(), q_rope.data_ptr(), c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap,
@@ -690,7 +698,7 @@ def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_s
                weights_out, dev_error)
     sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, cache_lens.shape[0])
     B, n, H, wi, wo, weights_out = _weights_args(q_abs, q_rope, cache_lens, vis, lse, path, length, weights_in,
-                                                 weights_out, M * page_size)
+                                                 weights_out, M * page_size, stream)
     _call_kv_attn_weights_paged(q_abs.data_ptr(), q_rope.data_ptr(), c_pages.data_ptr(), r_pages.data_ptr(), sc, sr,
         int(page_size), page_table.data_ptr(), M, N, cache_lens.data_ptr(), vis.data_ptr(), lse.data_ptr(),
         _addr(path), _addr(length), B, n, H, scale, _addr(weights_in), wi, weights_out.data_ptr(), wo,
@@ -698,19 +706,19 @@ def kd_kv_attn_weights_paged(q_abs, q_rope, c_pages, r_pages, page_table, page_s
     return weights_out
 
 
-def _evict_args(cache_lens, weights_in, cap, dst_cap, keep, inplace, weights_out, lens_out, kept):
+def _evict_args(cache_lens, weights_in, cap, dst_cap, keep, inplace, weights_out, lens_out, kept, stream):
     _typed(cache_lens, torch.int32, "cache_lens")
     B, dev = cache_lens.shape[0], cache_lens.device
     wi = _weight_rows(weights_in, B, cap, "weights_in")
     rows = min(dst_cap, max(int(keep), 1))
     if weights_out is None:
-        weights_out = weights_in if inplace else torch.zeros(B, dst_cap, dtype=torch.float32, device=dev)
+        weights_out = weights_in if inplace else _new(stream, torch.zeros, B, dst_cap, dtype=torch.float32, device=dev)
     wo = _weight_rows(weights_out, B, rows, "weights_out")
     if lens_out is None:
-        lens_out = cache_lens if inplace else torch.empty(B, dtype=torch.int32, device=dev)
+        lens_out = cache_lens if inplace else _new(stream, torch.empty, B, dtype=torch.int32, device=dev)
     _typed(lens_out, torch.int32, "lens_out", (B,))
     if kept is None:
-        kept = torch.empty(B, max(int(keep), 1), dtype=torch.int32, device=dev)
+        kept = _new(stream, torch.empty, B, max(int(keep), 1), dtype=torch.int32, device=dev)
     _typed(kept, torch.int32, "kept", (B, max(int(keep), 1)))
     return B, wi, wo, weights_out, lens_out, kept
 
@@ -730,7 +738,7 @@ def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_
         c_dst, r_dst = c_kv, k_rope
     drows, dc, dr, dcap = _cache(c_dst, r_dst)
     B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, cap, dcap, keep, inplace, weights_out,
-                                                         lens_out, kept)
+                                                         lens_out, kept, stream)
     if rows != B or drows != B:
         raise ValueError("the caches must hold B requests")
     _call_kv_evict(c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap, cache_lens.data_ptr(), weights_in.data_ptr(), wi,
@@ -757,7 +765,7 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
         c_dst, r_dst = c_pages, r_pages
     dc, dr, DM, DN = _pages(c_dst, r_dst, dst_page_table, page_size, cache_lens.shape[0])
     B, wi, wo, weights_out, lens_out, kept = _evict_args(cache_lens, weights_in, M * page_size, DM * page_size, keep,
-                                                         inplace, weights_out, lens_out, kept)
+                                                         inplace, weights_out, lens_out, kept, stream)
     _call_kv_evict_paged(c_pages.data_ptr(), r_pages.data_ptr(), sc, sr, int(page_size), page_table.data_ptr(), M, N,
         cache_lens.data_ptr(), weights_in.data_ptr(), wi, int(keep), int(sink), int(recent), B, c_dst.data_ptr(),
         r_dst.data_ptr(), dc, dr, dst_page_table.data_ptr(), DM, DN, weights_out.data_ptr(), wo, lens_out.data_ptr(),
