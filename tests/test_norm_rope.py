@@ -334,6 +334,14 @@ def test_write_device_errors(kd):
 
 
 @pytest.mark.gpu
+def test_write_refuses_no_requests_and_uneven_tokens(kd):
+    table, lens = table_of(10, 64), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for B, T in ((0, 0), (0, 3), (2, 3)):
+        with pytest.raises(ValueError):
+            kd.kd_kv_norm_rope_write(normal(B, 8, 512), normal(B, 8, 64), lens[:B], normal(T, 576), None, table)
+
+
+@pytest.mark.gpu
 def test_write_agrees_with_the_node_write(kd):
     """Without a norm and at position 0 the call is kd_kv_write_nodes, bit for bit."""
     B, n, cap = 3, 17, 40

@@ -553,7 +553,7 @@ def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
         _typed(kv_weight, torch.bfloat16, "kv_weight", (D_C,))
     if cu_seqlens is not None:
         _typed(cu_seqlens, torch.int32, "cu_seqlens", (B + 1,))
-    elif T % B:
+    elif B < 1 or T % B:
         raise ValueError("without cu_seqlens the tokens must divide evenly among the requests")
     H = qt = qh = 0
     if q_rope_in is not None:
