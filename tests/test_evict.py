@@ -372,6 +372,33 @@ def test_evict_many_requests_and_long(kd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,L,keep,page", [(40, 1500, 1100, 0), (40, 1500, 300, 64), (3, 6000, 4500, 0), (2, 4000, 3999, 16)])
+def test_evict_in_place_in_many_steps(kd, B, L, keep, page):
+    """Rows that move a little and rows that move far, over many steps of a CTA; few and many requests."""
+    Ls = [L - 7 * b for b in range(B)]
+    cap = L + 2
+    if page:
+        pt, pool = pages_for(B, cap, page, 1)
+        cap = pt.shape[1] * page
+        slots = torch.arange(cap)
+        rows = pt[:, slots // page] * page + slots % page
+    else:
+        pool, rows = B * cap, torch.arange(B * cap).view(B, cap)
+    c, r = normal(pool, 512, seed=1), normal(pool, 64, seed=2)
+    src = [x.view(torch.int16).cpu().clone() for x in (c, r)]
+    w = torch.from_numpy(np.random.default_rng(B).random((B, cap)).astype(np.float32))
+    w[:, : L // 2] += 0.5 * (torch.arange(B) % 2)[:, None]
+    lens, win = i32(Ls), w.cuda()
+    if page:
+        kept, wo, lo = kd.kd_kv_evict_paged(c, r, pt.int().cuda(), page, lens, win, keep, 4, 50)
+    else:
+        kept, wo, lo = kd.kd_kv_evict(c.view(B, cap, 512), r.view(B, cap, 64), lens, win, keep, 4, 50)
+    now = [x.view(torch.int16).cpu() for x in (c, r)]
+    check_evict(kept.cpu(), wo, lo.cpu(), Ls, w, keep, 4, 50, lambda b, s: [x[rows[b, s]] for x in src],
+                lambda b, s: [x[rows[b, s]] for x in now], None)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["equal", "random", "ties"])
 def test_evict_longer_than_a_cluster_reads_at_once(kd, kind):
     """Caches numbered in several steps (a cluster holds 32768 slots), with equal weights on both

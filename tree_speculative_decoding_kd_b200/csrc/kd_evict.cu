@@ -12,7 +12,7 @@
 // threads of 32 registers and four slots each took 2 us more, one CTA per request 66 us for
 // 32 K slots; rows already known to be kept prefetched into L2 during the passes cost 4 to 20.
 // The move copies the kept rows: bound by memory, 2 x 1152 bytes a row, 16 bytes per lane: 302
-// MB in 54 us, 5.6 TB/s.  It is launched with the selection still running (programmatic
+// MB in 46 us, 6.6 TB/s.  It is launched with the selection still running (programmatic
 // dependent launch) and waits for it on the device.
 
 #include "kd_common.cuh"
@@ -243,62 +243,70 @@ struct MoveParams {
 };
 constexpr int CC = KD_D_C / 8, CR = KD_D_R / 8;    // 16-byte pieces of a row
 
-// Another destination: a warp copies ROWS rows, all their loads in flight together.
-constexpr int ROWS = 4;
-__global__ void __launch_bounds__(256) move_kernel(const MoveParams p) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+// Another destination: a warp a row.  (Two, four and eight rows, their loads in flight together,
+// took 2, 9 and 17 us more for 302 MB: so many rows are on their way anyway that the memory does
+// better with them close together; stores that stay in the L2 cost another 2.)
+constexpr int ROWS = 8;                              // of a CTA
+__global__ void __launch_bounds__(32 * ROWS) move_kernel(const MoveParams p) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31, m = blockIdx.x * ROWS + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection is complete
-  const int m0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * ROWS;
-  const int32_t* kept = p.kept + (size_t)b * p.keep;
-  uint4 v[ROWS][2], x[ROWS];
-  bool on[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int s = m0 + i < p.keep ? kept[m0 + i] : -1;
-    on[i] = s >= 0;
-    if (!on[i]) continue;
-    const int64_t row = p.src.row(b, s);
-    v[i][0] = __ldcs(p.c + row * p.sc + lane);
-    v[i][1] = __ldcs(p.c + row * p.sc + lane + 32);
-    if (lane < CR) x[i] = __ldcs(p.r + row * p.sr + lane);
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (!on[i]) continue;
-    const int64_t row = p.dst.row(b, m0 + i);
-    p.cd[row * p.dc + lane] = v[i][0];
-    p.cd[row * p.dc + lane + 32] = v[i][1];
-    if (lane < CR) p.rd[row * p.dr + lane] = x[i];
-  }
+  const int s = m < p.keep ? p.kept[(size_t)b * p.keep + m] : -1;
+  if (s < 0) return;
+  const int64_t from = p.src.row(b, s), to = p.dst.row(b, m);
+  const uint4 v0 = __ldcs(p.c + from * p.sc + lane), v1 = __ldcs(p.c + from * p.sc + lane + 32);
+  uint4 x = {};
+  if (lane < CR) x = __ldcs(p.r + from * p.sr + lane);
+  __stcs(p.cd + to * p.dc + lane, v0);
+  __stcs(p.cd + to * p.dc + lane + 32, v1);
+  if (lane < CR) __stcs(p.rd + to * p.dr + lane, x);
 }
 
 // In place: a CTA takes one 64-byte column slice of every row (four 16-byte pieces; 16
 // slices of the latent, 2 of the rope key), so that rows of one slice move in order while
 // the slices need no order between them.  Rows move down (kept[m] >= m, ascending): once
 // the sources of rows [m0, m1) are read, nothing that is still to be read lies below row
-// m1, so each step reads its rows, waits for the whole CTA to have read, and writes.
-constexpr int SLICES = (CC + CR) / 4, STEP = 8;
-__global__ void __launch_bounds__(512) move_inplace_kernel(const MoveParams p) {
-  const int b = blockIdx.y, sl = blockIdx.x, piece = threadIdx.x & 3, r = threadIdx.x >> 2;
+// m1, so each step reads its rows, waits for the whole CTA to have read, and writes.  The next
+// step's reads, all from m1 on, are on their way meanwhile, as are the numbers of the one after.
+constexpr int PIECES = 4, SLICES = (CC + CR) / PIECES;
+template <int SIZE, int STEP>                          // threads, rows of a thread and step
+__global__ void __launch_bounds__(SIZE) move_inplace_kernel(const MoveParams p) {
+  constexpr int AT_ONCE = SIZE / PIECES;
+  const int b = blockIdx.y, sl = blockIdx.x, piece = threadIdx.x % PIECES, r = threadIdx.x / PIECES;
   const int32_t* kept = p.kept + (size_t)b * p.keep;
-  const bool lat = sl < CC / 4;
-  uint4* base = lat ? p.cd + sl * 4 + piece : p.rd + (sl - CC / 4) * 4 + piece;
+  const bool lat = sl < CC / PIECES;
+  uint4* base = lat ? p.cd + sl * PIECES + piece : p.rd + (sl - CC / PIECES) * PIECES + piece;
   const int64_t stride = lat ? p.dc : p.dr;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection is complete
-  for (int m0 = 0; m0 < p.keep; m0 += 128 * STEP) {
-    uint4 v[STEP];
-    int s[STEP];
+  // sources of the step at m0, -1 where nothing moves
+  auto look = [&](int m0, int (&s)[STEP]) {
 #pragma unroll
     for (int i = 0; i < STEP; ++i) {
-      const int m = m0 + i * 128 + r;
+      const int m = m0 + i * AT_ONCE + r;
       s[i] = m < p.keep ? kept[m] : -1;
       if (s[i] == m) s[i] = -1;                        // already in place
-      if (s[i] >= 0) v[i] = base[p.src.row(b, s[i]) * stride];
     }
-    __syncthreads();
+  };
+  auto read = [&](const int (&s)[STEP], uint4 (&v)[STEP]) {
 #pragma unroll
     for (int i = 0; i < STEP; ++i)
-      if (s[i] >= 0) base[p.dst.row(b, m0 + i * 128 + r) * stride] = v[i];
+      if (s[i] >= 0) v[i] = base[p.src.row(b, s[i]) * stride];
+  };
+  int s[STEP], s1[STEP], s2[STEP];
+  uint4 v[STEP], v1[STEP];
+  look(0, s);
+  look(STEP * AT_ONCE, s1);
+  read(s, v);
+  for (int m0 = 0; m0 < p.keep; m0 += STEP * AT_ONCE) {
+    look(m0 + 2 * STEP * AT_ONCE, s2);
+    read(s1, v1);                                      // lies behind every row written so far, and in this step
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+      if (s[i] >= 0) base[p.dst.row(b, m0 + i * AT_ONCE + r) * stride] = v[i];
+      s[i] = s1[i];
+      s1[i] = s2[i];
+      v[i] = v1[i];
+    }
   }
 }
 
@@ -363,9 +371,19 @@ static int evict_impl(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc
   m.keep = keep;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = inplace ? dim3(ev::SLICES, B) : dim3((unsigned)((keep + 8 * ev::ROWS - 1) / (8 * ev::ROWS)), B);
-  cfg.blockDim = dim3(inplace ? 512 : 256);
-  return cuda_status(cudaLaunchKernelEx(&cfg, inplace ? ev::move_inplace_kernel : ev::move_kernel, m), "move_kernel");
+  if (!inplace) {
+    cfg.gridDim = dim3((unsigned)((keep + ev::ROWS - 1) / ev::ROWS), B);
+    cfg.blockDim = dim3(32 * ev::ROWS);
+    return cuda_status(cudaLaunchKernelEx(&cfg, ev::move_kernel, m), "move_kernel");
+  }
+  // Small CTAs where there are enough of them, else large ones that have more rows on their way: 64
+  // caches of 9000 slots to 2048 take 76 and 87 us, 8 of 32768 to 16384 102 and 80 (140 and 137
+  // by 512 threads of eight rows without reading ahead).
+  const bool many = (int64_t)ev::SLICES * B >= 4 * (int64_t)sms;
+  cfg.gridDim = dim3(ev::SLICES, B);
+  cfg.blockDim = dim3(many ? 256 : 1024);
+  return cuda_status(cudaLaunchKernelEx(&cfg, many ? ev::move_inplace_kernel<256, 4> : ev::move_inplace_kernel<1024, 2>, m),
+                     "move_inplace_kernel");
 }
 
 // Whether the memory of two sets of rows (width elements each) meets.
