@@ -4,13 +4,15 @@
 // Two launches.  select_kernel (a cluster of up to 8 CTAs per request) finds the weight of
 // the last slot that is kept, by a radix selection over order-preserving 32-bit keys (11 +
 // 11 + 10 bits, a histogram in shared memory each, added up across the cluster through
-// distributed shared memory), and then walks the slots in order once, numbering the kept
-// ones: equal weights are taken from the lowest slot.  It is bound by latency: about 17 us,
-// 4 for each pass (histogram 0.8, cluster barrier 0.9, 57 KB of the others' histograms 1 to 2,
-// scan 0.3) and 4 for the numbering; where a pass ends on a digit whose keys are all kept, the
-// rest is left out (64 requests without equal weights: 76 to 73 us with the move).  1024
-// threads of 32 registers and four slots each took 2 us more, one CTA per request 66 us for
-// 32 K slots; rows already known to be kept prefetched into L2 during the passes cost 4 to 20.
+// distributed shared memory; where at most 4096 keys share the first digit, every CTA fetches
+// those and goes on by itself), and then walks the slots in order once, numbering the kept
+// ones: equal weights are taken from the lowest slot.  It is bound by latency: about 15 us, 4 for
+// a pass of the cluster (histogram 0.8, cluster barrier 0.9, 57 KB of the others' histograms 1
+// to 2, scan 0.3), 5 for the other two by itself and 4 for the numbering; where a pass ends on a
+// digit whose keys are all kept, the rest is left out.  Measured: three passes of the cluster 1 to
+// 2 us more; 1024 threads of 32 registers and four slots each another 2; one CTA per request 66
+// us for 32 K slots; rows already known to be kept prefetched into L2 during the passes 4 to 20
+// more.
 // The move copies the kept rows: bound by memory, 2 x 1152 bytes a row, 16 bytes per lane: 302
 // MB in 46 us, 6.6 TB/s.  It is launched with the selection still running (programmatic
 // dependent launch) and waits for it on the device.
@@ -27,6 +29,7 @@ constexpr int BINS = 2048;
 constexpr int PER = 8;                       // neighbouring slots a thread numbers per step
 constexpr int CHUNK = THREADS * PER;         // slots a CTA works on per step
 constexpr int MAXC = 8;                      // CTAs of a cluster
+constexpr int FEW = 4096;                    // keys of one first digit that every CTA goes on with by itself
 
 // Unsigned key in the order of the weights: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -84,7 +87,8 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
 __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p, const int cs) {
   __shared__ __align__(16) uint32_t hist[3][BINS];
   __shared__ uint32_t warp_sums[WARPS];
-  __shared__ uint32_t found[3], totals[2];
+  __shared__ uint32_t found[3], totals[2], counts[MAXC];
+  __shared__ uint32_t list[FEW], listed;
   asm volatile("griddepcontrol.launch_dependents;");      // the move may come up and wait
   const int b = blockIdx.x / cs, tid = threadIdx.x;
   const int rank = cs > 1 ? (int)ptx::cluster_ctarank() : 0;
@@ -125,35 +129,13 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p
   if (L > p.keep && p.keep > p.sink + p.recent) {
     need = (uint32_t)(p.keep - p.sink - p.recent);
     for (int i = tid; i < 3 * BINS; i += THREADS) (&hist[0][0])[i] = 0u;
+    if (tid == 0) listed = 0u;
     __syncthreads();
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
+    // The next digit, from its histogram: thread t has the bins 2047 - 4t to 2044 - 4t, `h` their
+    // counts, the largest digit's first: sums run from that.  True when every key of the digit is
+    // kept: the rest does not matter.
+    auto pick = [&](int pass, const uint32_t (&h)[4]) -> bool {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digits = pass == 2 ? 1023u : 2047u;
-#pragma unroll 1
-      for (int step = 0; step < steps; ++step) {
-        if (steps > 1) load(step);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int j = step * span + j0 + i;
-          const uint32_t key = order_key(v[i]);
-          if (j >= first && j < last && (key & mask) == thr) atomicAdd(&hist[pass][(key >> shift) & digits], 1u);
-        }
-      }
-      if (cs > 1) {
-        __syncthreads();
-        ptx::cluster_sync();
-      } else {
-        __syncthreads();
-      }
-      // thread t holds the bins 2047 - 4t to 2044 - 4t: sums run from the largest digit
-      const uint32_t at = ptx::smem_u32(&hist[pass][BINS - 4 - 4 * tid]);
-      uint32_t h[4] = {0u, 0u, 0u, 0u};                // of the largest digit first
-      for (int r = 0; r < cs; ++r) {                   // the others', from the next one on
-        const int q = rank + r < cs ? rank + r : rank + r - cs;
-        const uint4 o = cs > 1 ? ld_cluster_v4(ptx::map_to_rank(at, (uint32_t)q)) : ptx::ld_shared_v4(at);
-        h[0] += o.w, h[1] += o.z, h[2] += o.y, h[3] += o.x;
-      }
       uint32_t total;
       const uint32_t mine = (h[0] + h[1]) + (h[2] + h[3]);
       uint32_t above = block_scan(mine, warp_sums, total) - mine;
@@ -169,8 +151,78 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const SelectParams p
       __syncthreads();
       thr |= found[0] << shift;
       need = found[1];
-      mask |= digits << shift;
-      if (found[2] == need) break;                     // every key of the digit is kept: the rest does not matter
+      mask |= (pass == 2 ? 1023u : 2047u) << shift;
+      return found[2] == need;
+    };
+    auto counted = [&](int pass, uint32_t (&h)[4]) {   // the bins of this CTA
+      const uint4 o = *reinterpret_cast<const uint4*>(&hist[pass][BINS - 4 - 4 * tid]);
+      h[0] = o.w, h[1] = o.z, h[2] = o.y, h[3] = o.x;
+    };
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+#pragma unroll 1
+      for (int step = 0; step < steps; ++step) {
+        if (steps > 1) load(step);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int j = step * span + j0 + i;
+          const uint32_t key = order_key(v[i]);
+          if (j >= first && j < last && (key & mask) == thr) atomicAdd(&hist[pass][(key >> shift) & digits], 1u);
+        }
+      }
+      __syncthreads();
+      if (cs > 1) ptx::cluster_sync();
+      uint32_t h[4];
+      counted(pass, h);
+      const uint32_t at = ptx::smem_u32(&hist[pass][BINS - 4 - 4 * tid]);
+      for (int r = 1; r < cs; ++r) {                   // the others', from the next one on
+        const int q = rank + r < cs ? rank + r : rank + r - cs;
+        const uint4 o = ld_cluster_v4(ptx::map_to_rank(at, (uint32_t)q));
+        h[0] += o.w, h[1] += o.z, h[2] += o.y, h[3] += o.x;
+      }
+      if (pick(pass, h)) break;
+      if (pass > 0 || cs == 1 || found[2] > (uint32_t)FEW) continue;
+
+      // Few keys have that digit: every CTA looks at all of them and goes on without the others.
+      const uint32_t few = found[2];
+#pragma unroll 1
+      for (int step = 0; step < steps; ++step) {
+        if (steps > 1) load(step);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int j = step * span + j0 + i;
+          const uint32_t key = order_key(v[i]);
+          if (j >= first && j < last && (key & mask) == thr) list[atomicAdd(&listed, 1u)] = key;
+        }
+      }
+      __syncthreads();
+      ptx::cluster_sync();
+      if (tid < cs) counts[tid] = ld_cluster_u32(ptx::map_to_rank(ptx::smem_u32(&listed), (uint32_t)tid));
+      __syncthreads();
+      uint32_t key[FEW / THREADS];
+#pragma unroll
+      for (int i = 0; i < FEW / THREADS; ++i) {
+        uint32_t n = tid + i * THREADS;
+        if (n < few) {
+          int r = 0;
+          while (r < cs - 1 && n >= counts[r]) n -= counts[r++];
+          key[i] = ld_cluster_u32(ptx::map_to_rank(ptx::smem_u32(&list[min(n, FEW - 1u)]), (uint32_t)r));
+        }
+      }
+#pragma unroll 1
+      for (int next = 1; next < 3; ++next) {
+        const int low = next == 1 ? 10 : 0;
+#pragma unroll
+        for (int i = 0; i < FEW / THREADS; ++i)
+          if (tid + i * THREADS < (int)few && (key[i] & mask) == thr)
+            atomicAdd(&hist[next][(key[i] >> low) & (next == 1 ? 2047u : 1023u)], 1u);
+        __syncthreads();
+        counted(next, h);
+        if (pick(next, h)) break;
+      }
+      break;
     }
   }
   const bool all = L <= p.keep, none = !all && p.keep == p.sink + p.recent;
