@@ -544,7 +544,8 @@ int kd_kv_attn_weights_paged(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* 
  * Limits: keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep, cap <= 2^31 - 1.
  * The paged form goes through page tables (any page_size >= 1, the same for both): in
  * place when the destination's pools and table are the source's, else the
- * destination's pages must be none of the source's.  A page id outside its pool among
+ * destination's pages must be none of the source's.  No page that is written may be
+ * another request's too: requests that share a prefix's pages go elsewhere.  A page id outside its pool among
  * the slots read or written sets KD_DEV_BAD_PAGE, and the request is treated as above.
  */
 int kd_kv_evict(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t kv_row_stride_c,

@@ -752,7 +752,8 @@ def kd_kv_evict_paged(c_pages, r_pages, page_table, page_size, cache_lens, weigh
                       dev_error=None, stream=None):
     """kd_kv_evict through page tables: in place without dst_page_table (the request's tail
     pages are then free), else into the pages of dst_page_table (of c_dst, r_dst, or of the
-    same pool), which must be none of the source's."""
+    same pool), which must be none of the source's.  Requests that share pages (a common prefix)
+    are evicted into pages of their own, not in place."""
     dev = _on_device(c_pages, r_pages, page_table, cache_lens, weights_in, c_dst, r_dst, dst_page_table, weights_out,
                lens_out, kept, dev_error)
     sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, cache_lens.shape[0])
