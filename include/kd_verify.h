@@ -541,7 +541,8 @@ int kd_kv_attn_weights_paged(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* 
  * which are then no longer cache_lens + i.
  * A request with L < 0, L > cap or lens_out > dst_cap sets KD_DEV_CACHE_FULL; its kept
  * row is -1 and nothing else of it is written.
- * Limits: keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep, cap <= 2^31 - 1.
+ * Limits: keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep; keep and both
+ * capacities at most 2^30.
  * The paged form goes through page tables (any page_size >= 1, the same for both): in
  * place when the destination's pools and table are the source's, else the
  * destination's pages must be none of the source's.  No page that is written may be

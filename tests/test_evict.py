@@ -129,6 +129,19 @@ def test_host_validation(lib):
         assert lib.kd_kv_evict_paged(*bad) == -1, i
 
 
+def test_evict_refuses_more_slots_than_it_numbers(lib):
+    """keep and the capacities up to 2^30: beyond, a 32-bit number of a step's last slot would wrap."""
+    V, M = ctypes.c_void_p, 1 << 44
+    ok = [V(16), V(M), 512, 64, 1 << 30, V(16), V(16), 1 << 31, 50, 1, 1, 1, V(2 * M), V(3 * M), 512, 64, 1 << 30, V(16),
+          1 << 31, V(16), V(16), None, None]
+    if not torch.cuda.is_available():                   # refused for want of a device, not for the arguments
+        assert lib.kd_kv_evict(*ok) not in (-1, 0)
+    for i, v in ((4, (1 << 30) + 1), (8, (1 << 30) + 1), (8, (1 << 31) - 1), (16, (1 << 30) + 1), (16, (1 << 31) - 1)):
+        bad = list(ok)
+        bad[i] = v
+        assert lib.kd_kv_evict(*bad) == -1, i
+
+
 def test_reference_selection():
     assert ref_keep([5, 1, 3, 3, 9, 3], 6, 4, 1, 1) == [0, 2, 4, 5]
     assert ref_keep([0, math.nan, -math.inf, -0.0, 0.0, 0], 6, 4, 1, 1) == [0, 3, 4, 5]

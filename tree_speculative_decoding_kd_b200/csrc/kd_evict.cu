@@ -29,6 +29,7 @@ constexpr int BINS = 2048;
 constexpr int PER = 8;                       // neighbouring slots a thread numbers per step
 constexpr int CHUNK = THREADS * PER;         // slots a CTA works on per step
 constexpr int MAXC = 8;                      // CTAs of a cluster
+constexpr int MOST = 1 << 30;                // slots of a request: 32-bit numbers have room for a step more
 constexpr int FEW = 4096;                    // keys of one first digit that every CTA goes on with by itself
 
 // Unsigned key in the order of the weights: NaN lowest, -0 equal to +0.
@@ -375,7 +376,7 @@ static int evict_impl(const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t sc
                       cudaStream_t stream) {
   if (!cache_ok(c_kv, k_rope, sc, sr, src.cap) || !cache_ok(c_dst, r_dst, dc, dr, dst.cap) || !cache_lens || !w_in ||
       !w_out || !lens_out || !kept || B < 1 || B > 65535 || keep < 1 || sink < 0 || recent < 0 ||
-      (int64_t)sink + recent > keep || src.cap > INT32_MAX || dst.cap > INT32_MAX || wi < src.cap ||
+      (int64_t)sink + recent > keep || keep > ev::MOST || src.cap > ev::MOST || dst.cap > ev::MOST || wi < src.cap ||
       wo < (dst.cap < keep ? dst.cap : keep) || (w_out == w_in && wi != wo))
     return KD_EINVAL;
   int sms = 0, st = device_sms(&sms);
