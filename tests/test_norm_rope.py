@@ -353,3 +353,46 @@ def test_write_agrees_with_the_node_write(kd):
     kd.kd_kv_norm_rope_write(c, r, L, kv, pos, table_of(4, 64))
     kd.kd_kv_write_nodes(c2, r2, L, kv[:, :512].reshape(B, n, 512).contiguous(), kv[:, 512:].reshape(B, n, 64).contiguous())
     assert torch.equal(c.view(torch.int16), c2.view(torch.int16)) and torch.equal(r.view(torch.int16), r2.view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("cu", [[0, 8, 4], [0, 5, 3, 8], [0, 4, 8, 6, 8], [0, 5, 12], [0, 8, 9], [0, -1, 8], [1, 4, 8],
+                                [0] * 200 + [8, 7] + [8] * 150, [0] * 300 + [8] * 50 + [9]])
+def test_write_with_bad_cumulative_lengths_leaves_everything(kd, cu, page):
+    """One bad entry anywhere, also of a request without tokens: its bit is set and neither the
+    cache nor the queries are touched."""
+    B, T, H = len(cu) - 1, 8, 3
+    c, r, pt, _ = cache(kd, B, 32, page, False, 0)
+    kv, q = normal(T, 576, seed=1), normal(T, H, 64, seed=2)
+    qo, err = torch.full((T, H, 64), 9.0, dtype=torch.bfloat16, device="cuda"), kd.new_error_word()
+    L = torch.zeros(B, dtype=torch.int32, device="cuda")
+    more = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), q_rope_in=q, q_rope_out=qo, dev_error=err)
+    if page:
+        kd.kd_kv_norm_rope_write_paged(c, r, pt, page, L, kv, None, table_of(64, 64), **more)
+    else:
+        kd.kd_kv_norm_rope_write(c, r, L, kv, None, table_of(64, 64), **more)
+    assert kd.decode_device_error(kd.kd_read_device_error(err)) == ["BAD_SEQLENS"]
+    assert bool((c == 5.0).all()) and bool((r == 5.0).all()) and bool((qo == 9.0).all())
+
+
+@pytest.mark.gpu
+def test_write_of_many_ragged_requests(kd):
+    """More requests than a block has threads, many of them without tokens, rows behind the last one."""
+    lens = [(b * b) % 4 if b % 3 else 0 for b in range(700)]
+    B, T, cap = len(lens), sum(lens), 8
+    c, r, _, _ = cache(kd, B, cap, 0, False, 0)
+    kv, w, table, err = normal(T + 5, 576, seed=1), normal(512, seed=2), table_of(16, 64), kd.new_error_word()
+    past = [b % 5 for b in range(B)]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    kd.kd_kv_norm_rope_write(c, r, torch.tensor(past, dtype=torch.int32, device="cuda"), kv, None, table, cu_seqlens=cu,
+                             kv_weight=w, eps=EPS, dev_error=err)
+    assert kd.kd_read_device_error(err) == 0
+    at = [past[b] + i for b, n in enumerate(lens) for i in range(n)]
+    where = torch.tensor([b * cap + past[b] + i for b, n in enumerate(lens) for i in range(n)], device="cuda")
+    y, x = ref_norm(kv[:T, :512], w), kv[:T, 512:].double()
+    within(c.view(-1, 512)[where], y, y)
+    within(r.view(-1, 64)[where], ref_rotate(x, torch.tensor(at, device="cuda"), table, True), x)
+    other = torch.ones(B * cap, dtype=torch.bool, device="cuda")
+    other[where] = False
+    assert bool((c.view(-1, 512)[other] == 5.0).all()) and bool((r.view(-1, 64)[other] == 5.0).all())

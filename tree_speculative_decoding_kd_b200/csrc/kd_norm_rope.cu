@@ -263,6 +263,19 @@ __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const Write
   const int lane = threadIdx.x & 31;
   const unsigned wi = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
   const unsigned t = wi / (unsigned)p.items, item = wi - t * (unsigned)p.items;
+  if (p.cu) {
+    // cumulative lengths: all of them, by every block; a bad one ends the call (a token's search
+    // over an unsorted array can end on an interval that looks right)
+    bool bad = false;
+    for (int i = threadIdx.x; i < p.B; i += THREADS) {
+      const int a = p.cu[i], z = p.cu[i + 1];
+      bad |= (i == 0 && a != 0) || a < 0 || z < a || z > p.T;
+    }
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0 && blockIdx.x == 0) raise_dev_error(p.err, KD_DEV_BAD_SEQLENS);
+      return;
+    }
+  }
   if (t >= (unsigned)p.T) return;
   int b, first, count;
   if (p.cu) {
@@ -270,10 +283,6 @@ __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const Write
     if (b == p.B) return;                                    // behind the last sequence
     first = p.cu[b];
     count = p.cu[b + 1] - first;
-    if (first < 0 || (int)t < first || (int)t - first >= count || p.cu[b + 1] > p.T) {
-      if (lane == 0) raise_dev_error(p.err, KD_DEV_BAD_SEQLENS);
-      return;
-    }
   } else {
     b = (int)(t / (unsigned)p.n);
     first = b * p.n;
