@@ -422,7 +422,8 @@ int kd_qk_norm_rope(const kd_bf16_t* q, int64_t q_tok_stride, int64_t q_head_str
  *   contiguous; both NULL with H = 0 to write the cache alone.  q_rope_out may be
  *   q_rope_in when that is contiguous.
  * cache_lens is not changed.  A request with cache_lens + length > cap (or < 0) sets
- * KD_DEV_CACHE_FULL and none of its rows is written; cumulative lengths that do not start
+ * KD_DEV_CACHE_FULL, whatever its tokens' positions are, and none of its rows is written
+ * (without positions, slots below 0 are bad positions too); cumulative lengths that do not start
  * at 0, decrease or pass T anywhere set KD_DEV_BAD_SEQLENS, and nothing is written, the
  * queries' part included.  The queries' part does not depend on
  * the cache: it is written for every token of a sequence with a valid position.

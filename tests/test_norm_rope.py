@@ -396,3 +396,29 @@ def test_write_of_many_ragged_requests(kd):
     other = torch.ones(B * cap, dtype=torch.bool, device="cuda")
     other[where] = False
     assert bool((c.view(-1, 512)[other] == 5.0).all()) and bool((r.view(-1, 64)[other] == 5.0).all())
+
+
+@pytest.mark.gpu
+def test_write_reports_a_bad_length_beside_bad_positions(kd):
+    """A length below 0 or past the capacity is reported whatever the tokens' positions are; nothing
+    of that request is cached, and the queries are written where the position is valid."""
+    B, n, H, cap, table, w = 2, 4, 2, 32, table_of(40, 64), normal(512, seed=3)
+    kv, q = normal(B * n, 576, seed=1), normal(B * n, H, 64, seed=2)
+    x = q.double()
+    for first, pos, bits, live in (
+            (-5, None, {"CACHE_FULL", "BAD_POSITION"}, []), (-2, None, {"CACHE_FULL", "BAD_POSITION"}, [2, 3]),
+            (-5, [3, 4, 5, 6], {"CACHE_FULL"}, [0, 1, 2, 3]), (30, [-1, -1, 40, 99], {"CACHE_FULL", "BAD_POSITION"}, []),
+            (30, [0, 1, 40, 2], {"CACHE_FULL", "BAD_POSITION"}, [0, 1, 3])):
+        c, r, _, _ = cache(kd, B, cap, 0, False, 0)
+        qo, err = torch.full((B * n, H, 64), 9.0, dtype=torch.bfloat16, device="cuda"), kd.new_error_word()
+        p = None if pos is None else torch.tensor(pos + [7, 8, 9, 10], dtype=torch.int32, device="cuda")
+        kd.kd_kv_norm_rope_write(c, r, torch.tensor([first, 7], dtype=torch.int32, device="cuda"), kv, p, table,
+                                 kv_weight=w, eps=EPS, q_rope_in=q, q_rope_out=qo, dev_error=err)
+        assert set(kd.decode_device_error(kd.kd_read_device_error(err))) == bits
+        assert bool((c[0] == 5.0).all()) and bool((r[0] == 5.0).all())
+        y = ref_norm(kv[n:, :512], w)
+        within(c[1, 7:7 + n], y, y)
+        at = torch.tensor(pos or [first + i for i in range(n)], device="cuda")
+        within(qo[live], ref_rotate(x[live], at[live], table, True), x[live])
+        dead = [i for i in range(n) if i not in live]
+        assert bool((qo[dead] == 9.0).all())

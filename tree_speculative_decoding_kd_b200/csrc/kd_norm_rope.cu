@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const Write
     count = p.n;
   }
   const int64_t L = p.lens[b], slot = L + ((int)t - first);
+  const bool full = L < 0 || L + count > p.map.cap;          // reported whatever the position is
+  if (full && item == 0 && lane == 0) raise_dev_error(p.err, KD_DEV_CACHE_FULL);
   const int64_t at = p.pos ? (int64_t)p.pos[t] : slot;
   if (at < 0 || at >= p.max_pos) {
     if (lane == 0) raise_dev_error(p.err, KD_DEV_BAD_POSITION);
@@ -321,12 +323,9 @@ __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const Write
       rr[1] = *reinterpret_cast<const uint4*>(src + KD_D_C + eb);
     }
     turn.load(row, ea, eb, KD_D_R, true, p.inter != 0);
-    int bad = 0;
-    if (L < 0 || L + count > p.map.cap) bad = KD_DEV_CACHE_FULL;
-    else if (!p.map.pages_ok(b, slot, slot + 1)) bad = KD_DEV_BAD_PAGE;
-    if (bad) {
-      if (lane == 0) raise_dev_error(p.err, bad);
-    } else {
+    const bool stored = !full && p.map.pages_ok(b, slot, slot + 1);
+    if (!full && !stored && lane == 0) raise_dev_error(p.err, KD_DEV_BAD_PAGE);
+    if (stored) {
       const int64_t r = p.map.row(b, slot);
       float x[2][8], ss = 0.f;
 #pragma unroll
