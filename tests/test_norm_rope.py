@@ -422,3 +422,49 @@ def test_write_reports_a_bad_length_beside_bad_positions(kd):
         within(qo[live], ref_rotate(x[live], at[live], table, True), x[live])
         dead = [i for i in range(n) if i not in live]
         assert bool((qo[dead] == 9.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,page", [(4099, 20, 0), (9000, 3, 16), (6000, 0, 0)])
+def test_write_of_thousands_of_requests(kd, B, H, page):
+    """So many that a block takes several tokens: every row and query as with one, errors of single
+    requests among them; a decrease at the far end ends the call."""
+    lens = [1 + (b % 7 == 3) - (b % 11 == 5) for b in range(B)]
+    T, cap, n_bad = sum(lens), 8, [17, B - 2]
+    past = [b % 5 for b in range(B)]
+    for b in n_bad:
+        past[b] = -(-cap // page) * page if page else cap    # no room
+    c, r, pt, rows = cache(kd, B, cap, page, False, 0)
+    kv, w, table, err = normal(T + 3, 576, seed=1), normal(512, seed=2), table_of(32, 64), kd.new_error_word()
+    q = normal(T + 3, H, 64, seed=3) if H else None
+    qo = torch.full((T + 3, H, 64), 9.0, dtype=torch.bfloat16, device="cuda") if H else None
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    L = torch.tensor(past, dtype=torch.int32, device="cuda")
+
+    def write(cu):
+        more = dict(cu_seqlens=cu, kv_weight=w, eps=EPS, q_rope_in=q, q_rope_out=qo, dev_error=err)
+        if page:
+            kd.kd_kv_norm_rope_write_paged(c, r, pt, page, L, kv, None, table, **more)
+        else:
+            kd.kd_kv_norm_rope_write(c, r, L, kv, None, table, **more)
+        return kd.decode_device_error(kd.kd_read_device_error(err))
+
+    wrong = cu.clone()
+    wrong[B - 1] = T + 1
+    assert write(wrong) == ["BAD_SEQLENS"]
+    cf, rf = c.reshape(-1, 512), r.reshape(-1, 64)
+    assert bool((cf == 5.0).all()) and bool((rf == 5.0).all()) and (not H or bool((qo == 9.0).all()))
+    assert write(cu) == ["CACHE_FULL"]
+    tok = [(b, i) for b, n in enumerate(lens) for i in range(n)]
+    ok = [t for t, (b, _) in enumerate(tok) if b not in n_bad]
+    where = torch.tensor([int(rows[tok[t][0], past[tok[t][0]] + tok[t][1]]) for t in ok], device="cuda")
+    at = torch.tensor([past[b] + i for b, i in tok], device="cuda")
+    y, x = ref_norm(kv[ok, :512], w), kv[ok, 512:].double()
+    within(cf[where], y, y)
+    within(rf[where], ref_rotate(x, at[ok], table, True), x)
+    other = torch.ones(cf.shape[0], dtype=torch.bool, device="cuda")
+    other[where] = False
+    assert bool((cf[other] == 5.0).all()) and bool((rf[other] == 5.0).all())
+    if H:
+        within(qo[:T], ref_rotate(q[:T].double(), at, table, True), q[:T].double())
+        assert bool((qo[T:] == 9.0).all())

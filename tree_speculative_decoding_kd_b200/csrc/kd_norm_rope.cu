@@ -254,29 +254,11 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
   return lo;
 }
 
-// One warp per item of a token: item i the rope parts of `per` query heads from per i on (four
+// A warp's work: item i of a token is the rope parts of `per` query heads from per i on (four
 // lanes a head, eight heads at a time), item 0 the token's latent and rope key too, whose
 // loads are on their way with the queries' first ones.
-__global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const WriteParams p) {
-  __shared__ uint4 pieces[DEPTH * 2 * THREADS];
-  const Ring ring(pieces);
+__device__ __forceinline__ void write_item(const WriteParams& p, const Ring& ring, unsigned t, unsigned item) {
   const int lane = threadIdx.x & 31;
-  const unsigned wi = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
-  const unsigned t = wi / (unsigned)p.items, item = wi - t * (unsigned)p.items;
-  if (p.cu) {
-    // cumulative lengths: all of them, by every block; a bad one ends the call (a token's search
-    // over an unsorted array can end on an interval that looks right)
-    bool bad = false;
-    for (int i = threadIdx.x; i < p.B; i += THREADS) {
-      const int a = p.cu[i], z = p.cu[i + 1];
-      bad |= (i == 0 && a != 0) || a < 0 || z < a || z > p.T;
-    }
-    if (__syncthreads_or(bad)) {
-      if (threadIdx.x == 0 && blockIdx.x == 0) raise_dev_error(p.err, KD_DEV_BAD_SEQLENS);
-      return;
-    }
-  }
-  if (t >= (unsigned)p.T) return;
   int b, first, count;
   if (p.cu) {
     b = sequence_of(p.cu, p.B, (int)t);
@@ -372,6 +354,29 @@ __global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const Write
     turn.apply(a, b);
     *reinterpret_cast<uint4*>(out + ea) = pack8(a);
     *reinterpret_cast<uint4*>(out + eb) = pack8(b);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS) kv_norm_rope_write_kernel(const WriteParams p) {
+  __shared__ uint4 pieces[DEPTH * 2 * THREADS];
+  const Ring ring(pieces);
+  if (p.cu) {
+    // cumulative lengths: all of them, by every block; a bad one ends the call (a token's search
+    // over an unsorted array can end on an interval that looks right)
+    bool bad = false;
+    for (int i = threadIdx.x; i < p.B; i += THREADS) {
+      const int a = p.cu[i], z = p.cu[i + 1];
+      bad |= (i == 0 && a != 0) || a < 0 || z < a || z > p.T;
+    }
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0 && blockIdx.x == 0) raise_dev_error(p.err, KD_DEV_BAD_SEQLENS);
+      return;
+    }
+  }
+  const unsigned all = (unsigned)p.T * (unsigned)p.items, step = gridDim.x * (THREADS / 32);
+  for (unsigned i = blockIdx.x * (THREADS / 32) + threadIdx.x / 32; i < all; i += step) {
+    const unsigned t = i / (unsigned)p.items;
+    write_item(p, ring, t, i - t * (unsigned)p.items);
   }
 }
 
@@ -479,7 +484,11 @@ static int write_impl(kd_bf16_t* c_kv, kd_bf16_t* k_rope, int64_t sc, int64_t sr
   while (p.per > 8 && (int64_t)T * ((H + p.per - 1) / p.per) < (int64_t)sms * 8) p.per /= 2;
   p.items = H > p.per ? (H + p.per - 1) / p.per : 1;
   p.inter = interleaved;
-  const unsigned grid = (unsigned)(((int64_t)T * p.items + nr::THREADS / 32 - 1) / (nr::THREADS / 32));
+  unsigned grid = (unsigned)(((int64_t)T * p.items + nr::THREADS / 32 - 1) / (nr::THREADS / 32));
+  // Every block reads all cumulative lengths: of thousands of requests, so many that it pays to have
+  // no more blocks than fit at once and several tokens for each (8192 requests of a token 15 us
+  // against 19 with a block for every four tokens, 65536 104 against 402; 4096 10 and 10).
+  if (cu && B >= 4096 && grid > (unsigned)sms * 7) grid = (unsigned)sms * 7;
   nr::kv_norm_rope_write_kernel<<<grid, nr::THREADS, 0, stream>>>(p);
   return launch_status("kv_norm_rope_write_kernel");
 }
