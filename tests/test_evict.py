@@ -536,6 +536,28 @@ def test_evict_within_one_pool(kd):
     assert torch.equal(pool[0][still], was[still])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [0, 16])
+def test_evict_lengths_of_failed_requests_are_zero(kd, page):
+    """Into another cache, lens_out made by the binding: a request that fails holds nothing there."""
+    B, cap, keep = 4, 64, 30
+    c, r, w = normal(B, cap, 512, seed=1), normal(B, cap, 64, seed=2), torch.rand(B, cap, device="cuda")
+    d, e = torch.zeros(B, 32, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, 32, 64, dtype=torch.bfloat16, device="cuda")
+    lens = i32([50, -1, 65, 20])
+    dirty = [torch.full((B,), 7, dtype=torch.int32, device="cuda") for _ in range(64)]      # what the allocator hands out next
+    torch.cuda.synchronize()
+    del dirty
+    if page:
+        pt = i32([[4 * b + i for i in range(4)] for b in range(B)])
+        dpt = i32([[2 * b + i for i in range(2)] for b in range(B)])
+        kept, _, lo = kd.kd_kv_evict_paged(c.view(-1, 512), r.view(-1, 64), pt, 16, lens, w, keep, 1, 2, c_dst=d.view(-1, 512),
+                                           r_dst=e.view(-1, 64), dst_page_table=dpt)
+    else:
+        kept, _, lo = kd.kd_kv_evict(c, r, lens, w, keep, 1, 2, c_dst=d, r_dst=e)
+    assert lo.tolist() == [30, 0, 0, 20] and lens.tolist() == [50, -1, 65, 20]
+    assert bool((kept[1:3] == -1).all()) and bool((d[1:3] == 0).all())
+
+
 # ------------------------------------------------------------------ together
 def test_names_in_the_header():
     import os

@@ -715,7 +715,8 @@ def _evict_args(cache_lens, weights_in, cap, dst_cap, keep, inplace, weights_out
         weights_out = weights_in if inplace else _new(stream, torch.zeros, B, dst_cap, dtype=torch.float32, device=dev)
     wo = _weight_rows(weights_out, B, rows, "weights_out")
     if lens_out is None:
-        lens_out = cache_lens if inplace else _new(stream, torch.empty, B, dtype=torch.int32, device=dev)
+        # (zeros: a request that fails is not written, and holds nothing at its destination)
+        lens_out = cache_lens if inplace else _new(stream, torch.zeros, B, dtype=torch.int32, device=dev)
     _typed(lens_out, torch.int32, "lens_out", (B,))
     if kept is None:
         kept = _new(stream, torch.empty, B, max(int(keep), 1), dtype=torch.int32, device=dev)
@@ -728,7 +729,8 @@ def kd_kv_evict(c_kv, k_rope, cache_lens, weights_in, keep, sink=0, recent=0, c_
     """Cuts every request's cache to at most `keep` slots: its first `sink`, its last `recent`
     and those of the largest weights between.  Without c_dst, r_dst it works in place (cache,
     cache_lens and weights_in are updated); with them the kept rows go to another cache.
-    Returns (kept [B][keep] int32, weights_out, lens_out)."""
+    Returns (kept [B][keep] int32, weights_out, lens_out); in another cache the length of a
+    request that fails is 0 (one given is left as it was)."""
     dev = _on_device(c_kv, k_rope, cache_lens, weights_in, c_dst, r_dst, weights_out, lens_out, kept, dev_error)
     rows, sc, sr, cap = _cache(c_kv, k_rope)
     if (c_dst is None) != (r_dst is None):
