@@ -137,3 +137,66 @@ def test_overlapping_calls_on_two_streams(kd):
                     assert torch.equal(x[j, :L + 17], y[j, :L + 17])
             else:
                 assert torch.equal(x, y), i
+
+
+def test_calls_in_flight_at_once_on_two_streams(kd):
+    """Every call enqueued on two streams in turn, with nothing waited for until both are full: the
+    same bits as one after the other, and the streams did run at the same time."""
+    lens, B, n, H, cap, keep = [700, 33, 1500], 3, 17, 16, 2000, 300
+    T, Ls = sum(lens), (1900, 900, 40)
+
+    def made(seed):
+        q, k, v, kr, _ = inputs(lens, lens, 4, 4, True, seed=seed)
+        t = [tree(n, seed + b) for b in range(B)]
+        s = dict(q=q, k=k, v=v, kr=kr, cu=cu_of(lens), qa=normal(B, n, H, 512, seed=seed), qr=normal(B, n, H, 64, seed=seed + 1),
+                 c=normal(B, cap, 512, seed=seed + 2), r=normal(B, cap, 64, seed=seed + 3), lens=i32(Ls),
+                 vis=torch.from_numpy(np.stack([x[1] for x in t]).view(np.int32)).cuda(),
+                 lse=torch.full((B, n, H), 9.0, device="cuda"), w0=torch.rand(B, cap, device="cuda"),
+                 kv=normal(T, 576, seed=seed + 4), w=normal(512, seed=seed + 5), zero=i32([0] * B),
+                 table=table_of(cap, 64), table2=table_of(cap, 128), pos=torch.arange(T, device="cuda", dtype=torch.int32) % cap)
+        return s
+
+    def outputs():
+        def bf(*a):
+            return torch.zeros(*a, dtype=torch.bfloat16, device="cuda")
+        return dict(out=bf(T, 4, 128), lse=torch.zeros(T, 4, device="cuda"), w=torch.zeros(B, cap, device="cuda"),
+                    c=bf(B, 400, 512), r=bf(B, 400, 64), wo=torch.zeros(B, 400, device="cuda"), lo=i32([0] * B),
+                    kept=i32([[0] * keep] * B), c2=bf(B, 1600, 512), r2=bf(B, 1600, 64), q2=bf(T, 4, 64), heads=bf(T, 4, 128),
+                    keys=bf(T, 4, 128), err=kd.new_error_word())
+
+    def step(s, o, st):
+        kd.kd_qk_norm_rope(s["q"][..., :128], s["k"], s["pos"], s["table2"], q_out=o["heads"], k_out=o["keys"], dev_error=o["err"],
+                           stream=st)
+        kd.kd_kv_norm_rope_write(o["c2"], o["r2"], s["zero"], s["kv"], None, s["table"], cu_seqlens=s["cu"], kv_weight=s["w"],
+                                 q_rope_in=s["q"][..., 128:], q_rope_out=o["q2"], dev_error=o["err"], stream=st)
+        kd.kd_prompt_attn(o["heads"], o["keys"], s["v"], s["cu"], q_rope=o["q2"], k_rope=s["kr"], out=o["out"], lse=o["lse"],
+                          dev_error=o["err"], stream=st)
+        kd.kd_kv_attn_weights(s["qa"], s["qr"], s["c"], s["r"], s["lens"], s["vis"], s["lse"], weights_in=s["w0"],
+                              weights_out=o["w"], dev_error=o["err"], stream=st)
+        kd.kd_kv_evict(s["c"], s["r"], s["lens"], o["w"], keep, 4, 32, c_dst=o["c"], r_dst=o["r"], weights_out=o["wo"],
+                       lens_out=o["lo"], kept=o["kept"], dev_error=o["err"], stream=st)
+
+    sets = [made(1), made(20)]
+    want = [outputs() for _ in sets]
+    for s, o in zip(sets, want):                        # one after the other
+        for _ in range(2):
+            step(s, o, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [outputs() for _ in sets]
+    begin, end = ([torch.cuda.Event(enable_timing=True) for _ in sets] for _ in range(2))
+    torch.cuda.synchronize()
+    for st, e in zip(streams, begin):
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(40_000_000)               # about 20 ms: both queues fill meanwhile
+        e.record(st)
+    for _ in range(30):
+        for s, o, st in zip(sets, got, streams):
+            step(s, o, st)
+    for st, e in zip(streams, end):
+        e.record(st)
+    torch.cuda.synchronize()
+    assert begin[0].elapsed_time(end[1]) > 0 and begin[1].elapsed_time(end[0]) > 0       # neither ended before the other began
+    for a, b in zip(want, got):
+        assert kd.kd_read_device_error(a["err"]) == 0 and kd.kd_read_device_error(b["err"]) == 0
+        for name in a:
+            assert torch.equal(a[name], b[name]), name
