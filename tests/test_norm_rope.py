@@ -468,3 +468,44 @@ def test_write_of_thousands_of_requests(kd, B, H, page):
     if H:
         within(qo[:T], ref_rotate(q[:T].double(), at, table, True), q[:T].double())
         assert bool((qo[T:] == 9.0).all())
+
+
+def any_stride(x, axes):
+    """x with a stride of 3 along its axes of length 1: never used, as after a transpose of one column."""
+    assert all(x.shape[a] == 1 for a in axes)
+    return x.as_strided(x.shape, [3 if a in axes else s for a, s in enumerate(x.stride())])
+
+
+@pytest.mark.gpu
+def test_strides_of_single_tokens_and_heads_do_not_matter(kd):
+    """One token, one head: torch gives an axis of length 1 any stride (a column transposed has 1)."""
+    table, table128, w = table_of(20, 64), table_of(20, 128), normal(512, seed=1)
+    one, lens = torch.tensor([5], dtype=torch.int32, device="cuda"), torch.tensor([3], dtype=torch.int32, device="cuda")
+    q, k, kv, qr = normal(1, 4, 128, seed=2), normal(1, 1, 128, seed=3), normal(576, 1, seed=4).t(), normal(1, 4, 64, seed=5)
+    assert kv.is_contiguous() and kv.stride(0) == 1
+    qo, ko = any_stride(torch.zeros_like(q), [0]), any_stride(torch.zeros_like(k), [0, 1])
+    kd.kd_qk_norm_rope(any_stride(q, [0]), any_stride(k, [0, 1]), one, table128, q_out=qo, k_out=ko)
+    want = kd.kd_qk_norm_rope(q, k, one, table128)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+
+    got = []
+    for a, b in ((kv, any_stride(qr, [0])), (kv.clone(memory_format=torch.contiguous_format).view(-1).view(1, 576), qr)):
+        c, r = torch.zeros(1, 9, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 9, 64, dtype=torch.bfloat16, device="cuda")
+        cp, rp, pt = torch.zeros_like(c[0, :8]), torch.zeros_like(r[0, :8]), torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+        x = kd.kd_kv_norm_rope_write(c, r, lens, a, None, table, kv_weight=w, q_rope_in=b)
+        y = kd.kd_kv_norm_rope_write_paged(cp, rp, pt, 4, lens, a, None, table, kv_weight=w, q_rope_in=b)
+        got.append((c, r, cp, rp, x, y))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and bool((a != 0).any())
+
+
+@pytest.mark.gpu
+def test_prompt_strides_of_single_tokens_and_heads_do_not_matter(kd):
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    q, k, v = normal(1, 1, 128, seed=1), normal(1, 1, 128, seed=2), normal(1, 1, 128, seed=3)
+    qr, kr = normal(1, 1, 64, seed=4), normal(1, 64, seed=5)
+    want = kd.kd_prompt_attn(q, k, v, cu, q_rope=qr, k_rope=kr)
+    odd = [any_stride(x, [0, 1]) for x in (q, k, v, qr)]
+    for rope in (any_stride(kr, [0]), any_stride(kr.view(1, 1, 64), [0, 1])):
+        got = kd.kd_prompt_attn(odd[0], odd[1], odd[2], cu, q_rope=odd[3], k_rope=rope)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

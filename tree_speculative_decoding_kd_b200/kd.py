@@ -454,7 +454,8 @@ def _typed(t, dtype, name, shape=None):
 
 
 def _heads(t, name, tokens=None, heads=None, width=None):
-    """Shape and token and head strides of a bf16 [tokens][heads][width] view (unit stride inside a head)."""
+    """Shape and token and head strides of a bf16 [tokens][heads][width] view (unit stride inside a head;
+    0 for an axis of length 1, whose stride torch leaves arbitrary)."""
     if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name} must be bf16 [tokens][heads][width]")
     T, H, D = t.shape
@@ -465,7 +466,7 @@ def _heads(t, name, tokens=None, heads=None, width=None):
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have unit stride inside a head")
-    return T, H, D, st, sh
+    return T, H, D, st if T > 1 else 0, sh if H > 1 else 0
 
 
 def _cache(c, r):
@@ -546,6 +547,7 @@ def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
     if kv.dtype is not torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != D_C + D_R or kv.stride(1) != 1:
         raise ValueError("kv must be bf16 [T][576] with unit-stride rows")
     T = kv.shape[0]
+    row = kv.stride(0) if T > 1 else D_C + D_R
     max_pos, _ = _rope_table(rope_table, D_R)
     if positions is not None:
         _typed(positions, torch.int32, "positions", (T,))
@@ -563,7 +565,7 @@ def _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
         _typed(q_rope_out, torch.bfloat16, "q_rope_out", (T, H, D_R))
     elif q_rope_out is not None:
         raise ValueError("q_rope_out without q_rope_in")
-    return B, T, max_pos, H, qt, qh, q_rope_out
+    return B, T, row, max_pos, H, qt, qh, q_rope_out
 
 
 def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens=None, B=None,
@@ -576,12 +578,12 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
     dev = _on_device(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in, q_rope_out,
                dev_error)
     rows, sc, sr, cap = _cache(c_kv, k_rope)
-    B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
-                                                       q_rope_in, q_rope_out, stream)
+    B, T, row, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens,
+                                                            B, q_rope_in, q_rope_out, stream)
     if rows != B:
         raise ValueError("the cache must hold B requests")
     _call_kv_norm_rope_write(c_kv.data_ptr(), k_rope.data_ptr(), sc, sr, cap, cache_lens.data_ptr(), kv.data_ptr(),
-        kv.stride(0), _addr(kv_weight), eps, rope_table.data_ptr(), max_pos, _addr(positions), interleaved,
+        row, _addr(kv_weight), eps, rope_table.data_ptr(), max_pos, _addr(positions), interleaved,
         _addr(cu_seqlens), B, T, _addr(q_rope_in), qt, qh, H, _addr(q_rope_out), _addr(dev_error),
         _stream_of(stream, dev))
     return q_rope_out
@@ -593,11 +595,11 @@ def kd_kv_norm_rope_write_paged(c_pages, r_pages, page_table, page_size, cache_l
     """kd_kv_norm_rope_write through a page table."""
     dev = _on_device(c_pages, r_pages, page_table, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in,
                q_rope_out, dev_error)
-    B, T, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens, B,
-                                                       q_rope_in, q_rope_out, stream)
+    B, T, row, max_pos, H, qt, qh, q_rope_out = _write_args(cache_lens, kv, positions, rope_table, kv_weight, cu_seqlens,
+                                                            B, q_rope_in, q_rope_out, stream)
     sc, sr, M, N = _pages(c_pages, r_pages, page_table, page_size, B)
     _call_kv_norm_rope_write_paged(c_pages.data_ptr(), r_pages.data_ptr(), sc, sr, int(page_size),
-        page_table.data_ptr(), M, N, cache_lens.data_ptr(), kv.data_ptr(), kv.stride(0), _addr(kv_weight), eps,
+        page_table.data_ptr(), M, N, cache_lens.data_ptr(), kv.data_ptr(), row, _addr(kv_weight), eps,
         rope_table.data_ptr(), max_pos, _addr(positions), interleaved, _addr(cu_seqlens), B, T, _addr(q_rope_in), qt,
         qh, H, _addr(q_rope_out), _addr(dev_error), _stream_of(stream, dev))
     return q_rope_out
