@@ -75,7 +75,7 @@ typedef uint16_t kd_bf16_t;
 #define KD_DEV_BAD_PARENT    0x01  /* parent[0] != -1 or parent[i] not in [0, i)       */
 #define KD_DEV_CACHE_FULL    0x02  /* cache_len + n (or + len) exceeds cap, or < 0     */
 #define KD_DEV_BAD_PATH      0x04  /* len not in [1, n] or path entry not in [0, n)     */
-#define KD_DEV_BAD_POSITION  0x08  /* positions[b][i] != cache_len[b] + depth(i)       */
+#define KD_DEV_BAD_POSITION  0x08  /* positions[b][i] != cache_len[b] + depth(i); rotations: outside the table */
 #define KD_DEV_TIMEOUT       0x10  /* a bounded wait inside a kernel gave up            */
 #define KD_DEV_BAD_MASK      0x20  /* a node's mask lacks bit 0 (root) or its own bit   */
 #define KD_DEV_BAD_PAGE      0x40  /* a paged cache's page id is outside the page pool  */
@@ -427,8 +427,8 @@ int kd_qk_norm_rope(const kd_bf16_t* q, int64_t q_tok_stride, int64_t q_head_str
  * at 0, decrease or pass T anywhere set KD_DEV_BAD_SEQLENS, and nothing is written, the
  * queries' part included.  The queries' part does not depend on
  * the cache: it is written for every token of a sequence with a valid position.
- * Limits: T >= 0, B >= 1, 0 <= H <= 128; alignment as kd_kv_write_nodes, strides
- * multiples of 8.
+ * Limits: 0 <= T <= 2^27 (0 enqueues nothing), B >= 1, 0 <= H <= 128; alignment as
+ * kd_kv_write_nodes, strides multiples of 8.
  * The paged form writes through a page table (any page_size >= 1); a token whose page
  * id lies outside the pool sets KD_DEV_BAD_PAGE and is not written.
  */
@@ -473,8 +473,8 @@ int kd_kv_norm_rope_write_paged(kd_bf16_t* c_pages, kd_bf16_t* r_pages, int64_t 
  * KD_DEV_BAD_SEQLENS, and nothing is written.
  * Limits: T, Tk >= 0 (T = 0 enqueues nothing), T H and Tk Hk <= 2^31 - 1,
  * 1 <= B <= 65535, 1 <= H <= 128, Hk divides H, scale > 0 and finite; pointers 16-byte
- * aligned (out: 32), strides multiples of 8, those of queries not 0; H (T / 256 + B)
- * <= 2^31 - 1.
+ * aligned (out: 32), strides multiples of 8 and not 0 but for axes of length 1 and the
+ * head strides of keys and values (0: one head for all).
  */
 int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qn_tok_stride, int64_t qn_head_stride,
                    const kd_bf16_t* q_rope, int64_t qr_tok_stride, int64_t qr_head_stride,
@@ -501,11 +501,12 @@ int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qn_tok_stride, int64_t qn_he
  *   weights_in [B][w_in_stride] fp32 or NULL (zeros), weights_out [B][w_out_stride]
  *   fp32, strides >= cap; weights_out may be weights_in (same stride).
  * Sums run in a fixed order: the same call gives the same bits.  A request with
- * cache_lens + n > cap (or < 0) sets KD_DEV_CACHE_FULL; len not in [1, n] or a path
- * entry outside [0, n) sets KD_DEV_BAD_PATH; (paged) a page id outside the pool among
- * its first ceil((L + n) / page_size) sets KD_DEV_BAD_PAGE: nothing of it is written.
- * Layouts, limits and alignment of the other arguments as kd_tree_verify_attn; the
- * paged form takes page_size 64, 128 or 256.
+ * cache_lens + n > cap (or < 0) sets KD_DEV_CACHE_FULL; else len not in [1, n] sets
+ * KD_DEV_BAD_PATH; else a path entry outside [0, n) sets KD_DEV_BAD_PATH and (paged) a page
+ * id outside the pool among its first ceil((L + n) / page_size) sets KD_DEV_BAD_PAGE:
+ * nothing of it is written.
+ * Layouts, limits and alignment of the other arguments as kd_tree_verify_attn, and
+ * B <= 65535; the paged form takes page_size 64, 128 or 256.
  */
 int kd_kv_attn_weights(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* q_rope,
                        const kd_bf16_t* c_kv, const kd_bf16_t* k_rope, int64_t kv_row_stride_c,
@@ -540,11 +541,12 @@ int kd_kv_attn_weights_paged(const kd_bf16_t* q_nope_absorbed, const kd_bf16_t* 
  *   strides and dst_cap == cap.  lens_out may be cache_lens, weights_out may be
  *   weights_in (same stride).
  * Keys carry their rotation with them: later tokens go on with their own positions,
- * which are then no longer cache_lens + i.
+ * which are then no longer cache_lens + i: kd_kv_norm_rope_write takes them from its
+ * `positions`, and kd_tree_verify_attn, which checks its own against cache_lens, takes NULL.
  * A request with L < 0, L > cap or lens_out > dst_cap sets KD_DEV_CACHE_FULL; its kept
  * row is -1 and nothing else of it is written.
- * Limits: keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep; keep and both
- * capacities at most 2^30.
+ * Limits: 1 <= B <= 65535, keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep; keep
+ * and both capacities at most 2^30; w_in_stride >= cap, w_out_stride >= min(keep, dst_cap).
  * The paged form goes through page tables (any page_size >= 1, the same for both): in
  * place when the destination's pools and table are the source's, else the
  * destination's pages must be none of the source's.  No page that is written may be

@@ -13,9 +13,9 @@
 // Shared memory is thirteen 16 KB stages of 64 columns: the unit's keys stay in nine of them,
 // the query rows pass through four.  A chunk of keys is refilled for the next unit as soon as
 // the last query tile has used it, so that with few rows (one query tile, as for an accepted
-// path: bound by the cache's bytes) the next unit's keys stream in behind this one's products.
-// Measured (one B200): 4 x 16384 keys against 8192 rows 465 us (1.34 PFLOP/s at the power
-// cap, 1.5 cold); the accepted paths of 64 requests 147 to 164 us (4.2 to 4.6 TB/s of keys;
+// path) the next unit's keys stream in behind this one's products.
+// Measured (one B200): 4 x 16384 keys against 8192 rows 455 to 481 us (1.3 to 1.37 PFLOP/s at the
+// power cap, 1.5 cold); the accepted paths of 64 requests 147 to 185 us (3.7 to 4.6 TB/s of keys;
 // 178 with the next tile's path looked up only when its turn came).
 // One CTA alone, with two 32 KB stages for the query rows, took 588 and 195 us.  Letting the
 // keys pass through 6, 8, 10 or 11 of the stages instead of keeping them cost 3 to 20% for the
@@ -593,7 +593,7 @@ static int weights_impl(const kd_bf16_t* qa, const kd_bf16_t* qr, const kd_bf16_
 
   // Pairs of a cluster: the number with the shortest longest run of query tiles, were every
   // request of length cap.  A path is short as a rule (acceptance ends within a few nodes), so
-  // it counts as at most four nodes.
+  // it counts as at most four nodes: a guess, not measured against paths that are long.
   const int64_t units = B * ((cap + aw::UK - 1) / aw::UK);
   const int nodes = path && n > 4 ? 4 : n;
   const int64_t qt = (nodes + p.per_tile - 1) / p.per_tile;

@@ -36,10 +36,10 @@
 // next unit's queries load and its scores begin while the last one's output is written.
 //
 // Measured (one B200, calls behind each other; the longer two at the 1000 W cap, 1.4 to 1.6
-// GHz): one prompt of 16384 tokens, 16 query heads on 2 key heads of 128: 1000 us (1.10
-// PFLOP/s, 1.29 in a call by itself); 4 prompts of 2000 to 3070 tokens, 64 heads of 192/128: 600
-// us (0.92, 1.11); 32 prompts of 1 to 300 tokens, 64 heads of 192/128: 86 us, where its inputs
-// and outputs are 352 MB, 54 us.  What bounds it: the chain of one tile (scores, maximum,
+// GHz): one prompt of 16384 tokens, 16 query heads on 2 key heads of 128: 980 to 1040 us (1.06 to
+// 1.12 PFLOP/s, 1.29 in a call by itself); 4 prompts of 2000 to 3070 tokens, 64 heads of 192/128:
+// 585 to 632 us (0.87 to 0.94, 1.11); 32 prompts of 1 to 300 tokens, 64 heads of 192/128: 86 to
+// 101 us, where its inputs and outputs are 352 MB, 54 us.  What bounds it: the chain of one tile (scores, maximum,
 // exponentials, the two products' hand-overs, about 2900 cycles a key tile where the products
 // of both tiles take 2050 to 2560), and the power cap.
 //
@@ -679,7 +679,8 @@ extern "C" int kd_prompt_attn(const kd_bf16_t* q_nope, int64_t qnt, int64_t qnh,
   // 32 prompts of 1 to 300 tokens, 28 heads on 4, 40 and 32 us; 8 of 1000 to 2000, 32 on 4, 193 and
   // 179; 27 of one or two tokens over 340 keys, 32 on 8, 45 and 20; but 4 of just 1024, 40 on 8,
   // 66 and 68.  Long ones leave few rows empty, and a tile's rows in one piece are faster: 4 of
-  // 4096 tokens, 16 heads on 2, 283 and 291, one of 16384 1016 and 1028.  Nor do groups share a
+  // 4096 tokens, 16 heads on 2, 283 and 291, one of 16384 1016 and 1028.  (2048 is between the
+  // lengths that gain and those that lose, neither by much: not a sharp bound.)  Nor do groups share a
   // tile that would leave an eighth of it empty (22 or more heads as a rule).
   const int group = H / Hk, full = pr::BM / group * group;
   const int packed = T < (int64_t)2048 * B && full >= pr::BM * 7 / 8 ? group : 1;

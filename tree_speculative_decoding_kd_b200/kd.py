@@ -514,7 +514,8 @@ def kd_qk_norm_rope(q, k, positions, rope_table, q_weight=None, k_weight=None, e
     """RMS norm of every head of q [T][H][D] and k [T][Hk][D] (k None: queries alone; a weight
     None: no norm) and the rotation of its elements [rot_offset, rot_offset + rot) by
     positions [T] int32; rope_table fp32 [max_pos][rot], cos | sin.  Returns (q_out, k_out),
-    allocated contiguous unless given; q_out=q, k_out=k works in place."""
+    allocated contiguous unless given (not cleared: a bad position's rows hold what was in
+    memory); q_out=q, k_out=k works in place."""
     dev = _on_device(q, k, positions, rope_table, q_weight, k_weight, q_out, k_out, dev_error)
     T, H, D, qt, qh = _heads(q, "q")
     _typed(positions, torch.int32, "positions", (T,))
@@ -574,7 +575,9 @@ def kd_kv_norm_rope_write(c_kv, k_rope, cache_lens, kv, positions, rope_table, c
     """Cache rows of new tokens from the down-projection's output kv [T][576]: the latent
     normed, the rope key rotated, both stored at slots cache_lens[b] + i; the queries' rope
     part q_rope_in [T][H][64] rotated beside them.  positions None: cache_lens[b] + i;
-    cu_seqlens None: T / B tokens per request.  Returns q_rope_out (None without queries)."""
+    cu_seqlens None: T / B tokens per request.  Returns q_rope_out (None without queries;
+    allocated unless given, and then not cleared: rows of bad positions or lengths, or behind
+    the last sequence, hold what was in memory)."""
     dev = _on_device(c_kv, k_rope, cache_lens, kv, positions, rope_table, cu_seqlens, kv_weight, q_rope_in, q_rope_out,
                dev_error)
     rows, sc, sr, cap = _cache(c_kv, k_rope)
@@ -612,7 +615,8 @@ def kd_prompt_attn(q_nope, k_nope, v, cu_seqlens_q, q_rope=None, k_rope=None, cu
     heads), any token and head strides; sequence b is rows cu_seqlens_q[b] .. [b + 1] of the
     queries and of the keys (cu_seqlens_k when those differ: the queries are the last
     positions).  scale None: 1 / sqrt(192) with a rope part, else 1 / sqrt(128).
-    Returns (out [T][H][128] bf16, lse [T][H] fp32)."""
+    Returns (out [T][H][128] bf16, lse [T][H] fp32), allocated unless given (not cleared: rows
+    behind the last sequence, and all with bad lengths, hold what was in memory)."""
     dev = _on_device(q_nope, k_nope, v, cu_seqlens_q, q_rope, k_rope, cu_seqlens_k, out, lse, dev_error)
     T, H, _, qnt, qnh = _heads(q_nope, "q_nope", None, None, 128)
     Tk, Hk, _, knt, knh = _heads(k_nope, "k_nope", None, None, 128)
