@@ -6,6 +6,9 @@
 // lanes), up to 256 query rows its N columns.  A thread of the epilogue then owns one key
 // and adds up along its own columns: no reduction between threads, no second product, a
 // fixed order.  With the rows' lse known, one pass is enough: nothing runs a maximum.
+// Scores are summed up in fp32 by the tensor core, in 36 steps, whose roundings make the weights
+// off by 4e-8 to 3.9e-6 of their 2-norm (fp32 products throughout: 3e-8 to 7e-7), most where
+// scores reach 20; scale and lse held as two floats each did not change that.
 //
 // Two CTAs work as a pair (cta_group::2): M = 256 keys, 128 in each CTA's shared memory,
 // while each CTA holds only half of the query rows.  The query rows then stream from L2 at

@@ -23,7 +23,8 @@
 // more than 8 (log2): P stays below 2^8 and O is rescaled rarely, by the softmax warps
 // themselves, between two products (the commit that announced S also covers every earlier
 // product into O).  The sum is kept in fp32 from the unrounded exponentials; the rounding of P
-// to bf16 is the type of the MMA's operand.
+// to bf16 is the type of the MMA's operand: outputs are off by 2.0e-3 of their 2-norm where fp32
+// products throughout give 1.6e-3, the output's own rounding to bf16.
 //
 // Shared memory: Q (two tiles of 128 rows), then a ring of 16 KB chunks through which keys
 // (128 keys x 64 columns) and values (64 keys x 128 columns) stream in the order they are
